@@ -10,6 +10,10 @@ C ABI's names (``include/lbsa.h``):
     row_ptr, col    = lbsa_blockset_export(bs)
     bits            = lbsa_blockset_export_bitmask(bs)          # [B,H,nB,ceil(nB/32)] block bits
     scores, out     = lbsa_score_attend(q, k, v, block)          # dense step: O and exact masses
+    table           = lbsa_rope_table((T, H, W), (44, 42, 42))  # cos, sin of the grid's three axes
+    q, k            = lbsa_rope([q, k], table, (T, H, W), (44, 42, 42), perm)
+    q, k, v         = lbsa_norm_rope([q, k, v], [wq, wk, None], table, (T, H, W), (44, 42, 42), perm)
+    dxs, dws        = lbsa_norm_rope_backward([dq, dk, dv], [q, k, v], [wq, wk, None], table, ...)
     perm            = lbsa_partition_perm(T, H, W, "3d", tile=(4, 4, 4))
     qp, kp, vp      = lbsa_permute([q, k, v], perm)
 
@@ -30,6 +34,7 @@ __all__ = [
     "lbsa_device_status", "lbsa_partition_perm", "lbsa_permute", "lbsa_selftest_wait", "lbsa_selftest_exp2", "lbsa_select_rule", "lbsa_score_attend",
     "lbsa_select_head_noalloc", "lbsa_select_tokens", "lbsa_select_routed", "lbsa_blockset_views",
     "lbsa_blockset_masks", "lbsa_blockset_export_bitmask", "lbsa_blockset_from_bitmask",
+    "lbsa_rope_table", "lbsa_rope", "lbsa_norm_rope", "lbsa_norm_rope_backward",
     "lbsa_last_error", "lbsa_version", "library_path", "load_library",
     "LBSA_OK", "LBSA_ERR_INVALID_ARG", "LBSA_ERR_UNSUPPORTED", "LBSA_ERR_CUDA", "LBSA_ERR_OOM",
     "LBSA_ERR_BAD_INDEX", "LBSA_ERR_INVALID_SCORES", "LBSA_ERR_TIMEOUT",
@@ -52,6 +57,18 @@ class _Desc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("N_valid", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64), ("stride_n", ctypes.c_int64)]
+
+
+class _RopePos(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("grid", ctypes.c_int32 * 3), ("dims", ctypes.c_int32 * 3),
+                ("layout", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _RopeItem(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("H", ctypes.c_int32), ("rotate", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("weight_heads", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3), ("dy_stride", ctypes.c_int64 * 3)]
 
 
 _LIB = None
@@ -94,6 +111,13 @@ def load_library():
         "lbsa_partition_perm": (ctypes.c_int, [I32, I32, I32, I32, I32, I32, I32, P, I32, P]),
         "lbsa_permute": (ctypes.c_int, [ctypes.POINTER(P), ctypes.POINTER(P), I32, P,
                                         ctypes.POINTER(_Desc), I32, P]),
+        "lbsa_rope_table": (ctypes.c_int, [ctypes.POINTER(I32), ctypes.POINTER(I32), D, ctypes.POINTER(D), P, P]),
+        "lbsa_rope": (ctypes.c_int, [ctypes.POINTER(_RopeItem), I32, I32, I32, I32, I32,
+                                     ctypes.POINTER(_RopePos), P, I32, P]),
+        "lbsa_norm_rope": (ctypes.c_int, [ctypes.POINTER(_RopeItem), I32, I32, I32, I32, I32,
+                                          ctypes.POINTER(_RopePos), P, D, P]),
+        "lbsa_norm_rope_backward": (ctypes.c_int, [ctypes.POINTER(_RopeItem), I32, I32, I32, I32, I32,
+                                                   ctypes.POINTER(_RopePos), P, D, P]),
         "lbsa_selftest_wait": (ctypes.c_int, [I64, P, P]),
         "lbsa_selftest_exp2": (ctypes.c_int, [P, P, I64, P]),
         "lbsa_select_head_noalloc": (ctypes.c_int, [P, I32, I32, I32, D, P, P, P, P]),
@@ -461,6 +485,119 @@ def lbsa_permute(xs, perm, inverse: bool = False, outs=None, stream=None):
     _check(load_library().lbsa_permute(xa, ya, n, _ptr(perm), ctypes.byref(desc), int(inverse),
                                        _stream(stream)))
     return outs
+
+
+_ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+
+
+def _three(values, name: str, ctype):
+    values = tuple(values)
+    if len(values) != 3:
+        raise LbsaError(LBSA_ERR_INVALID_ARG, f"{name} must have three entries (time, height, width)")
+    return (ctype * 3)(*values)
+
+
+def lbsa_rope_table(grid, dims, theta: float = 10000.0, start=(0.0, 0.0, 0.0), table=None, stream=None):
+    """The (cos, sin) table of a (T, H, W) token grid, fp32 [T*dt/2 + H*dh/2 + W*dw/2, 2]:
+    dims = (dt, dh, dw) elements of a row turn with each axis, start is the
+    position of the grid's origin (a later chunk of a streamed clip).  Angles
+    are computed in 64 bits."""
+    g, m = _three(grid, "grid", ctypes.c_int32), _three(dims, "dims", ctypes.c_int32)
+    n = max(sum(e * (r // 2) for e, r in zip(g, m)), 0)
+    if table is None:
+        table = torch.empty(n, 2, dtype=torch.float32, device=torch.device("cuda", torch.cuda.current_device()))
+    _on_device(table, "table", torch.float32, 2 * n)
+    _check(load_library().lbsa_rope_table(g, m, float(theta), _three(start, "start", ctypes.c_double), _ptr(table),
+                                          _stream(stream)))
+    return table
+
+
+def _rope_call(xs, ys, dys, weights, dweights, table, grid, dims, layout, perm):
+    """The arguments that lbsa_rope, lbsa_norm_rope and lbsa_norm_rope_backward share."""
+    n = len(xs)
+    if not 1 <= n <= 3 or len(ys) != n or len(weights) != n or (dys is not None and len(dys) != n):
+        raise LbsaError(LBSA_ERR_INVALID_ARG, "need 1..3 tensors, with as many weights (None: no norm), outputs and gradients")
+    items = (_RopeItem * n)()
+    first = xs[0]
+    if first.dim() != 4:
+        raise LbsaError(LBSA_ERR_INVALID_ARG, "expected [B, H, N, d] tensors")
+    B, _, N, d = first.shape
+    for i, x in enumerate(xs):
+        if x.dtype not in (torch.bfloat16, torch.float32):
+            raise LbsaError(LBSA_ERR_UNSUPPORTED, f"dtype {x.dtype}")
+        if x.dim() != 4 or (x.shape[0], x.shape[2], x.shape[3], x.dtype) != (B, N, d, first.dtype):
+            raise LbsaError(LBSA_ERR_INVALID_ARG, "tensors of one call must share B, N, d and dtype")
+        it, group = items[i], {"x": x, "y": ys[i]}
+        if dys is not None:
+            group["dy"] = dys[i]
+        for name, t in group.items():
+            _on_device(t, name, x.dtype, contiguous=False)
+            if t.shape != x.shape or t.stride(-1) != 1:
+                raise LbsaError(LBSA_ERR_INVALID_ARG, f"{name} must have x's shape and a contiguous last dim")
+            setattr(it, name, t.data_ptr())
+            setattr(it, name + "_stride", (ctypes.c_int64 * 3)(*(st if size > 1 else d for st, size in
+                                                                  zip(t.stride()[:3], t.shape[:3]))))
+        it.H, it.rotate = x.shape[1], int(weights[i] is not None or dweights is None)
+        w = weights[i]
+        if w is None:
+            continue
+        _on_device(w, "weight")
+        if w.dtype not in (torch.bfloat16, torch.float32) or w.shape not in ((d,), (x.shape[1], d)):
+            raise LbsaError(LBSA_ERR_INVALID_ARG, "a weight is bf16 or fp32, [d] or [H, d]")
+        it.weight, it.weight_dtype = w.data_ptr(), 0 if w.dtype == torch.bfloat16 else 1
+        it.weight_heads = 1 if w.dim() == 1 else x.shape[1]
+        if dweights:
+            it.dweight = dweights[i].data_ptr()
+    pos = None
+    if table is not None:
+        if grid is None or dims is None or layout not in _ROPE_LAYOUTS:
+            raise LbsaError(LBSA_ERR_INVALID_ARG, 'a rotation needs grid, dims and layout "interleaved" or "half"')
+        g, m = _three(grid, "grid", ctypes.c_int32), _three(dims, "dims", ctypes.c_int32)
+        _on_device(table, "table", torch.float32, max(sum(e * r for e, r in zip(g, m)), 0))
+        pos = ctypes.byref(_RopePos(table.data_ptr(), g, m, _ROPE_LAYOUTS[layout], 0))
+    _on_device(perm, "perm", torch.int32, N)
+    return items, n, B, N, d, 0 if first.dtype == torch.bfloat16 else 1, pos, _ptr(perm)
+
+
+def lbsa_rope(xs, table, grid, dims, perm=None, inverse: bool = False, layout: str = "interleaved", outs=None,
+              stream=None):
+    """Rotary positions over a (T, H, W) token grid for 1..3 tensors [B, H_i, N, d]
+    (the head counts may differ): the first sum(dims) elements of a row turn by
+    the token's time, height and width; tokens past the grid and elements past
+    sum(dims) stay as they are.  With perm (lbsa_partition_perm) the rows move
+    into block order in the same pass; inverse=True rotates back and scatters
+    the rows back, which is also the gradient."""
+    xs = list(xs)
+    outs = [torch.empty_like(x) for x in xs] if outs is None else list(outs)
+    args = _rope_call(xs, outs, None, [None] * len(xs), None, table, grid, dims, layout, perm)
+    _check(load_library().lbsa_rope(*args, int(inverse), _stream(stream)))
+    return outs
+
+
+def lbsa_norm_rope(xs, weights, table=None, grid=None, dims=None, perm=None, eps: float = 1e-6,
+                   layout: str = "interleaved", outs=None, stream=None):
+    """The per-head norm x / sqrt(mean(x^2) + eps) * weight of queries and keys,
+    their rotation (as lbsa_rope; without a table none) and the move into block
+    order, in one pass over 1..3 tensors [B, H_i, N, d].  A weight is [d] or
+    [H_i, d]; a tensor whose weight is None (values) is only moved."""
+    xs = list(xs)
+    outs = [torch.empty_like(x) for x in xs] if outs is None else list(outs)
+    args = _rope_call(xs, outs, None, list(weights), (), table, grid, dims, layout, perm)
+    _check(load_library().lbsa_norm_rope(*args, float(eps), _stream(stream)))
+    return outs
+
+
+def lbsa_norm_rope_backward(dys, xs, weights, table=None, grid=None, dims=None, perm=None, eps: float = 1e-6,
+                            layout: str = "interleaved", dxs=None, stream=None):
+    """Gradients of lbsa_norm_rope from those of its outputs (dys, in block order)
+    and its inputs: (dxs in source order, dweights fp32 with None where there is
+    no weight).  The same inputs give the same bits on every call."""
+    xs, weights = list(xs), list(weights)
+    dxs = [torch.empty_like(x) for x in xs] if dxs is None else list(dxs)
+    dws = [None if w is None else torch.empty(w.shape, dtype=torch.float32, device=w.device) for w in weights]
+    args = _rope_call(xs, dxs, list(dys), weights, dws, table, grid, dims, layout, perm)
+    _check(load_library().lbsa_norm_rope_backward(*args, float(eps), _stream(stream)))
+    return dxs, dws
 
 
 def lbsa_selftest_wait(limit_us: int = 1000, stream=None) -> int:

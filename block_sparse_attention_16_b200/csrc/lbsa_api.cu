@@ -201,6 +201,78 @@ int scratch_alloc(DeviceState* ds, size_t bytes, cudaStream_t s, Scratch* out) {
   return LBSA_OK;
 }
 
+int rope_pos(const lbsa_rope_pos* p, int d, lbsa::RopePos* out) {
+  if (!p->table) return fail(LBSA_ERR_INVALID_ARG, "rope table is NULL");
+  if (reinterpret_cast<uintptr_t>(p->table) & 7u) return fail(LBSA_ERR_INVALID_ARG, "rope table is not 8-byte aligned");
+  long long tokens = 1, dims = 0, entries = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (p->grid[i] < 1) return fail(LBSA_ERR_INVALID_ARG, "grid must be >= 1 in every axis");
+    if (p->dims[i] < 0 || p->dims[i] % 2) return fail(LBSA_ERR_INVALID_ARG, "rope dims must be even and >= 0");
+    if ((tokens *= p->grid[i]) >= (1ll << 31)) return fail(LBSA_ERR_INVALID_ARG, "grid too large");
+    dims += p->dims[i];
+    entries += static_cast<long long>(p->grid[i]) * (p->dims[i] / 2);
+  }
+  if (dims < 2 || dims > d) return fail(LBSA_ERR_INVALID_ARG, "rope dims sum to %lld: 2 .. %d wanted", dims, d);
+  if (entries >= (1ll << 31)) return fail(LBSA_ERR_INVALID_ARG, "rope table too large");
+  if (p->layout != LBSA_ROPE_INTERLEAVED && p->layout != LBSA_ROPE_HALF)
+    return fail(LBSA_ERR_INVALID_ARG, "rope layout %d", p->layout);
+  if (p->layout == LBSA_ROPE_HALF && dims % 16)
+    return fail(LBSA_ERR_UNSUPPORTED, "half-split pairs are built for rotated dims that are a multiple of 16 (%lld)", dims);
+  *out = lbsa::RopePos{reinterpret_cast<const float2*>(p->table), p->grid[0], p->grid[1], p->grid[2],
+                       p->dims[0], p->dims[1], p->dims[2], p->layout == LBSA_ROPE_HALF, static_cast<int>(tokens)};
+  return LBSA_OK;
+}
+
+int rope_tensor(const void* p, const char* name, const int64_t (&st)[3], int d, int es) {
+  int rc;
+  if ((rc = validate_ptr(p, name)) != LBSA_OK) return rc;
+  if (st[2] < d || st[1] < 1 || st[0] < 1)
+    return fail(LBSA_ERR_INVALID_ARG, "%s: strides (%lld, %lld, %lld) smaller than a row", name, (long long)st[0],
+                (long long)st[1], (long long)st[2]);
+  if ((st[0] * es) % 16 || (st[1] * es) % 16 || (st[2] * es) % 16)
+    return fail(LBSA_ERR_INVALID_ARG, "%s: byte strides must be multiples of 16", name);
+  return LBSA_OK;
+}
+
+int rope_items(const lbsa_rope_item* items, int count, int B, int N, int d, int dtype, const lbsa_rope_pos* pos,
+               bool backward, lbsa::RopeItem* out, lbsa::RopePos* p) {
+  int rc;
+  if (!items || count < 1 || count > 3) return fail(LBSA_ERR_INVALID_ARG, "need 1..3 tensors");
+  if (B < 1 || N < 1) return fail(LBSA_ERR_INVALID_ARG, "B and N must be >= 1 (got %d, %d)", B, N);
+  if (dtype != LBSA_BF16 && dtype != LBSA_F32) return fail(LBSA_ERR_INVALID_ARG, "dtype %d unknown", dtype);
+  if (d != 64 && d != 128) return fail(LBSA_ERR_UNSUPPORTED, "head dim %d: only 64 and 128 are built", d);
+  if (pos && (rc = rope_pos(pos, d, p)) != LBSA_OK) return rc;
+  const int es = dtype == LBSA_BF16 ? 2 : 4;
+  long long heads = 0;
+  for (int i = 0; i < count; ++i) {
+    const lbsa_rope_item& a = items[i];
+    if (a.H < 1) return fail(LBSA_ERR_INVALID_ARG, "H must be >= 1 (got %d)", a.H);
+    if ((rc = rope_tensor(a.y, backward ? "dx" : "y", a.y_stride, d, es)) != LBSA_OK) return rc;
+    if ((!backward || a.weight) && (rc = rope_tensor(a.x, "x", a.x_stride, d, es)) != LBSA_OK) return rc;
+    if (backward && (rc = rope_tensor(a.dy, "dy", a.dy_stride, d, es)) != LBSA_OK) return rc;
+    if (a.y == a.x || (backward && a.y == a.dy)) return fail(LBSA_ERR_INVALID_ARG, "input and output may not alias");
+    if (a.weight) {
+      if ((rc = validate_ptr(a.weight, "weight")) != LBSA_OK) return rc;
+      if (a.weight_dtype != LBSA_BF16 && a.weight_dtype != LBSA_F32)
+        return fail(LBSA_ERR_INVALID_ARG, "weight dtype %d unknown", a.weight_dtype);
+      if (a.weight_heads != 1 && a.weight_heads != a.H)
+        return fail(LBSA_ERR_INVALID_ARG, "weight has %d rows: 1 or H = %d wanted", a.weight_heads, a.H);
+      if (backward && (rc = validate_ptr(a.dweight, "dweight")) != LBSA_OK) return rc;
+    }
+    heads += static_cast<long long>(B) * a.H;
+    lbsa::RopeItem& o = out[i];
+    o = lbsa::RopeItem{a.x, a.y, a.dy, a.weight, a.dweight, a.H, pos && a.rotate, a.weight_dtype,
+                       a.weight ? a.weight_heads : 1, {}, {}, {}};
+    for (int k = 0; k < 3; ++k) {
+      o.xs[k] = a.x_stride[k];
+      o.ys[k] = a.y_stride[k];
+      o.ds[k] = a.dy_stride[k];
+    }
+  }
+  if (heads > 65535) return fail(LBSA_ERR_UNSUPPORTED, "%lld (batch, head) pairs over all tensors exceed 65535", heads);
+  return LBSA_OK;
+}
+
 long long wait_limit() { return lbsa::kDefaultWaitLimit; }
 
 int new_blockset(int B, int H, int nB, int block, int scope, double p, cudaStream_t s, lbsa_blockset** out) {
@@ -715,6 +787,75 @@ int lbsa_permute(const void* const* xs, void* const* ys, int32_t count, const in
   cudaError_t e =
       lbsa::launch_permute(xs, ys, count, perm, *desc, inverse, ds->status, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "lbsa_permute launch");
+  return LBSA_OK;
+}
+
+int lbsa_rope_table(const int32_t* grid, const int32_t* dims, double theta, const double* start, float* table,
+                    void* stream) {
+  int rc;
+  lbsa::RopePos pos;
+  if (!grid || !dims || !start) return fail(LBSA_ERR_INVALID_ARG, "grid, dims or start is NULL");
+  const lbsa_rope_pos p{table, {grid[0], grid[1], grid[2]}, {dims[0], dims[1], dims[2]}, LBSA_ROPE_INTERLEAVED, 0};
+  if ((rc = rope_pos(&p, 1 << 30, &pos)) != LBSA_OK) return rc;
+  if (!(theta > 0.0) || !std::isfinite(theta)) return fail(LBSA_ERR_INVALID_ARG, "theta = %g is not > 0", theta);
+  for (int i = 0; i < 3; ++i)
+    if (!std::isfinite(start[i])) return fail(LBSA_ERR_INVALID_ARG, "start[%d] is not finite", i);
+  cudaError_t e = lbsa::launch_rope_table(pos, theta, start, table, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "lbsa_rope_table launch");
+  return LBSA_OK;
+}
+
+int lbsa_rope(const lbsa_rope_item* items, int32_t count, int32_t B, int32_t N, int32_t d, int32_t dtype,
+              const lbsa_rope_pos* pos, const int32_t* perm, int32_t inverse, void* stream) {
+  int rc;
+  log_line("lbsa_rope count=%d B=%d N=%d d=%d dtype=%d inverse=%d", count, B, N, d, dtype, inverse);
+  lbsa::RopeItem it[3];
+  lbsa::RopePos p{};
+  if (!pos) return fail(LBSA_ERR_INVALID_ARG, "pos is NULL");
+  if ((rc = rope_items(items, count, B, N, d, dtype, pos, false, it, &p)) != LBSA_OK) return rc;
+  for (int i = 0; i < count; ++i)
+    if (it[i].weight) return fail(LBSA_ERR_INVALID_ARG, "lbsa_rope takes no weight (lbsa_norm_rope does)");
+  DeviceState* ds = nullptr;
+  if ((rc = device_state(&ds)) != LBSA_OK) return rc;
+  cudaError_t e = lbsa::launch_rope(it, count, B, N, d, dtype, p, perm, 0.f, inverse != 0, ds->status,
+                                    static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "lbsa_rope launch");
+  return LBSA_OK;
+}
+
+int lbsa_norm_rope(const lbsa_rope_item* items, int32_t count, int32_t B, int32_t N, int32_t d, int32_t dtype,
+                   const lbsa_rope_pos* pos, const int32_t* perm, double eps, void* stream) {
+  int rc;
+  log_line("lbsa_norm_rope count=%d B=%d N=%d d=%d dtype=%d eps=%g", count, B, N, d, dtype, eps);
+  lbsa::RopeItem it[3];
+  lbsa::RopePos p{};
+  if ((rc = rope_items(items, count, B, N, d, dtype, pos, false, it, &p)) != LBSA_OK) return rc;
+  if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(LBSA_ERR_INVALID_ARG, "eps = %g is not >= 0", eps);
+  DeviceState* ds = nullptr;
+  if ((rc = device_state(&ds)) != LBSA_OK) return rc;
+  cudaError_t e = lbsa::launch_rope(it, count, B, N, d, dtype, p, perm, static_cast<float>(eps), 0, ds->status,
+                                    static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "lbsa_norm_rope launch");
+  return LBSA_OK;
+}
+
+int lbsa_norm_rope_backward(const lbsa_rope_item* items, int32_t count, int32_t B, int32_t N, int32_t d,
+                            int32_t dtype, const lbsa_rope_pos* pos, const int32_t* perm, double eps, void* stream) {
+  int rc;
+  log_line("lbsa_norm_rope_backward count=%d B=%d N=%d d=%d dtype=%d eps=%g", count, B, N, d, dtype, eps);
+  lbsa::RopeItem it[3];
+  lbsa::RopePos p{};
+  if ((rc = rope_items(items, count, B, N, d, dtype, pos, true, it, &p)) != LBSA_OK) return rc;
+  if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(LBSA_ERR_INVALID_ARG, "eps = %g is not >= 0", eps);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  DeviceState* ds = nullptr;
+  Scratch ws;
+  if ((rc = device_state(&ds)) != LBSA_OK) return rc;
+  if ((rc = scratch_alloc(ds, lbsa::norm_rope_backward_workspace_bytes(it, count, B, N, d), s, &ws)) != LBSA_OK)
+    return rc;
+  cudaError_t e = lbsa::launch_norm_rope_backward(it, count, B, N, d, dtype, p, perm, static_cast<float>(eps), ws.ptr,
+                                                  ds->status, s);
+  if (e != cudaSuccess) return cuda_fail(e, "lbsa_norm_rope_backward launch");
   return LBSA_OK;
 }
 

@@ -145,6 +145,32 @@ cudaError_t launch_partition_perm(int T, int Hg, int Wg, int kind, int tt, int t
 cudaError_t launch_permute(const void* const* xs, void* const* ys, int count, const int32_t* perm,
                            const lbsa_qkv_desc& d, int inverse, int32_t* status, cudaStream_t s);
 
+// rotary positions and the per-head norm (rope.cu); strides are in elements: batch, head, row
+struct RopeItem {
+  const void* x;
+  void* y;                 // backward: the gradient of x
+  const void* dy;          // backward only
+  const void* weight;      // [weight_heads][d] or NULL: no norm
+  float* dweight;          // backward only
+  int H, rotate, weight_dtype, weight_heads;
+  int64_t xs[3], ys[3], ds[3];
+};
+struct RopePos {
+  const float2* table;     // (cos, sin): T x dt/2, then Hg x dh/2, then Wg x dw/2
+  int T, Hg, Wg, dt, dh, dw;
+  int half;                // pairs (i, i + rd/2) instead of (2i, 2i + 1)
+  int tokens;              // T * Hg * Wg; later tokens are not rotated
+};
+// (batch, head chunk) units a call splits into: the grid's y extent
+int rope_units(const RopeItem* items, int count, int B, int N, bool backward);
+cudaError_t launch_rope(const RopeItem* items, int count, int B, int N, int d, int dtype, const RopePos& pos,
+                        const int32_t* perm, float eps, int inverse, int32_t* status, cudaStream_t s);
+size_t norm_rope_backward_workspace_bytes(const RopeItem* items, int count, int B, int N, int d);
+cudaError_t launch_norm_rope_backward(const RopeItem* items, int count, int B, int N, int d, int dtype,
+                                      const RopePos& pos, const int32_t* perm, float eps, void* workspace,
+                                      int32_t* status, cudaStream_t s);
+cudaError_t launch_rope_table(const RopePos& pos, double theta, const double* start, float* table, cudaStream_t s);
+
 cudaError_t launch_selftest_wait(long long limit_ns, int32_t* out, cudaStream_t s);
 cudaError_t launch_selftest_exp2(const float* v, float* out, long long n, cudaStream_t s);
 

@@ -23,7 +23,10 @@
  *      the kept blocks and nothing else).
  * plus lbsa_permute / lbsa_partition_perm for the 1D / 2D / 3D block
  * partitions of the token grid (VMoBA review: layer-wise cyclic 1D-2D-3D
- * partition).
+ * partition), and what a layer has in front of it: rotary positions over the
+ * grid's three axes (lbsa_rope) and the per-head norm of queries and keys
+ * with that rotation (lbsa_norm_rope), both on the way into block order, with
+ * their gradients.
  *
  * Conventions shared by every call
  *   - Pointers named q, k, v, out, scores, lse, perm, x, y are DEVICE pointers
@@ -334,6 +337,80 @@ int lbsa_partition_perm(int32_t T, int32_t Hg, int32_t Wg, int32_t kind, int32_t
  * written twice (scatter).  x and y may not alias. */
 int lbsa_permute(const void* const* xs, void* const* ys, int32_t count, const int32_t* perm,
                  const lbsa_qkv_desc* desc, int32_t inverse, void* stream);
+
+/* Rotary positions over the token grid.  Token n of a (T, Hg, Wg) grid in
+ * raster order, n = (t*Hg + h)*Wg + w, has three positions.  The first
+ * rd = dt + dh + dw elements of a row form rd/2 pairs; pairs [0, dt/2) turn
+ * with the token's time, the next dh/2 with its height, the last dw/2 with its
+ * width: (a, b) -> (a cos - b sin, a sin + b cos).  Elements from rd on, and
+ * tokens from T*Hg*Wg on (text behind a clip), are left as they are. */
+typedef enum {
+  LBSA_ROPE_INTERLEAVED = 0,    /* pair i = elements (2i, 2i + 1)                  */
+  LBSA_ROPE_HALF = 1            /* pair i = elements (i, i + rd/2); rd % 16 == 0   */
+} lbsa_rope_layout;
+
+typedef struct {
+  const float* table;           /* device, lbsa_rope_table's layout: (cos, sin) of  */
+                                /* T x dt/2, then Hg x dh/2, then Wg x dw/2         */
+  int32_t grid[3];              /* T, Hg, Wg >= 1, product < 2^31                   */
+  int32_t dims[3];              /* dt, dh, dw: even, >= 0, sum in [2, d]            */
+  int32_t layout;               /* lbsa_rope_layout                                 */
+  int32_t reserved;
+} lbsa_rope_pos;
+
+/* One tensor [B, H, N, d] of a call; strides in elements, the d stride is 1;
+ * base pointers and byte strides are multiples of 16.  Tensors of one call may
+ * differ in H (shared key heads) and strides. */
+typedef struct {
+  const void* x;                /* input                                            */
+  void* y;                      /* output; backward: the gradient of x              */
+  const void* dy;               /* backward: gradient of the output, else ignored   */
+  const void* weight;           /* device [weight_heads][d] contiguous, 16-byte     */
+                                /* aligned, or NULL: no norm                        */
+  float* dweight;               /* backward: fp32 [weight_heads][d] out where       */
+                                /* weight is given, else ignored                    */
+  int32_t H;
+  int32_t rotate;               /* 0: this tensor takes no rotation                 */
+  int32_t weight_dtype;         /* lbsa_dtype of weight                             */
+  int32_t weight_heads;         /* 1 (one row for all heads) or H                   */
+  int64_t x_stride[3], y_stride[3], dy_stride[3];   /* batch, head, row             */
+} lbsa_rope_item;
+
+/* Fill the table: entry x of an axis with dim m holds the cosines and sines of
+ * (start + x) * theta^(-2i/m), i < m/2, computed in 64 bits and rounded to
+ * fp32.
+ *   grid, dims, start  host arrays of 3; start: any finite position of the
+ *                      grid's origin (a later chunk of a streamed clip)
+ *   theta              finite, > 0
+ *   table              device fp32, (T*dt + Hg*dh + Wg*dw) values */
+int lbsa_rope_table(const int32_t* grid, const int32_t* dims, double theta, const double* start, float* table,
+                    void* stream);
+
+/* Rotate 1..3 tensors (weight must be NULL), on the way into block order:
+ *   inverse == 0:  y[slot] = R(perm[slot]) x[perm[slot]]
+ *   inverse != 0:  y[perm[slot]] = R(perm[slot])^-1 x[slot]
+ * (perm NULL: slot order is raster order).  The inverse undoes the call and is
+ * its gradient.  perm as in lbsa_permute: an entry outside [0, N) skips its
+ * row and records LBSA_ERR_BAD_INDEX in the per-device status word.  x and y
+ * may not alias.  Products and sums in fp32, rounded once. */
+int lbsa_rope(const lbsa_rope_item* items, int32_t count, int32_t B, int32_t N, int32_t d, int32_t dtype,
+              const lbsa_rope_pos* pos, const int32_t* perm, int32_t inverse, void* stream);
+
+/* Norm of each row, weight, rotation and block order in one pass over 1..3
+ * tensors (queries, keys and, with neither norm nor rotation, values):
+ *   y[slot] = R(s) (w * x[s] / sqrt(mean(x[s]^2) + eps)),  s = perm[slot]
+ * An item without weight takes no norm, one without `rotate` (or a call
+ * without pos) no rotation.  eps >= 0. */
+int lbsa_norm_rope(const lbsa_rope_item* items, int32_t count, int32_t B, int32_t N, int32_t d, int32_t dtype,
+                   const lbsa_rope_pos* pos, const int32_t* perm, double eps, void* stream);
+
+/* Its gradients: y[s] = dL/dx[s] and dweight = dL/dw from dy (block order) and
+ * the same x (source order), weight, pos, perm and eps.  dweight is summed in
+ * a fixed order (fp32 within a block of rows, 64 bits across blocks), so
+ * repeated calls give the same bits.  Scratch: one fp32 row of d for each block
+ * of the launch (about 1,200), from the library pool. */
+int lbsa_norm_rope_backward(const lbsa_rope_item* items, int32_t count, int32_t B, int32_t N, int32_t d,
+                            int32_t dtype, const lbsa_rope_pos* pos, const int32_t* perm, double eps, void* stream);
 
 /* Self-test of the bounded-wait machinery: one kernel waits on an mbarrier
  * that nothing completes, gives up after `limit_us` microseconds of wall time

@@ -34,12 +34,16 @@ Modules
   select_routed  head_entropy, route_heads, select_routed (EG-Sparse
               entropy-routed competition domains)    (pinned)
   partition   raster / 1D / 2D / 3D token orders       (pinned)
+  attention_grad  sparse_attention_grad                (pinned)
+  rope        rope_angles, rope_rotate, norm_rope, norm_rope_grad   (pinned)
 
 Every function is pinned by a ``-m "not gpu"`` test against something other
 than itself (library routines, closed forms, brute force, hand-worked
 examples under ``tests/golden/``); none is "parity unpinned".
 """
 from .attention import dense_attention, sparse_attention, token_sparse_attention
+from .attention_grad import sparse_attention_grad
+from .rope import rope_angles, rotate as rope_rotate, norm_rope, norm_rope_grad
 from .scores import block_mass, meanpool_scores, token_meanpool_scores
 from .select import (select_contract, select_fp64, InvalidScores, threshold_fixed_point,
                      csr_rows, csr_from_rows)
@@ -54,6 +58,7 @@ __all__ = [
     "select_contract", "select_fp64", "InvalidScores", "threshold_fixed_point",
     "csr_rows", "csr_from_rows", "select_local_topk", "select_topp_floor", "floor_of_head",
     "head_entropy", "route_heads", "select_routed",
+    "sparse_attention_grad", "rope_angles", "rope_rotate", "norm_rope", "norm_rope_grad",
     "perm_raster", "perm_1d_temporal", "perm_2d_frame_tiles", "perm_3d_tiles",
     "perm_for_call", "PARTITION_CYCLE",
 ]
