@@ -7,6 +7,7 @@ C ABI's names (``include/lbsa.h``):
     scores          = lbsa_score(q, k, block, mode="exact")      # [B,H,nB,nB] fp32
     bs              = lbsa_select(scores, block, p=0.99, scope="row")
     out             = lbsa_attend(q, k, v, bs)                  # same shape/dtype as q
+    dq, dk, dv      = lbsa_attend_backward(q, k, v, bs, out, lse, dout)
     row_ptr, col    = lbsa_blockset_export(bs)
     bits            = lbsa_blockset_export_bitmask(bs)          # [B,H,nB,ceil(nB/32)] block bits
     scores, out     = lbsa_score_attend(q, k, v, block)          # dense step: O and exact masses
@@ -34,7 +35,7 @@ __all__ = [
     "lbsa_device_status", "lbsa_partition_perm", "lbsa_permute", "lbsa_selftest_wait", "lbsa_selftest_exp2", "lbsa_select_rule", "lbsa_score_attend",
     "lbsa_select_head_noalloc", "lbsa_select_tokens", "lbsa_select_routed", "lbsa_blockset_views",
     "lbsa_blockset_masks", "lbsa_blockset_export_bitmask", "lbsa_blockset_from_bitmask",
-    "lbsa_rope_table", "lbsa_rope", "lbsa_norm_rope", "lbsa_norm_rope_backward",
+    "lbsa_attend_backward", "lbsa_rope_table", "lbsa_rope", "lbsa_norm_rope", "lbsa_norm_rope_backward",
     "lbsa_last_error", "lbsa_version", "library_path", "load_library",
     "LBSA_OK", "LBSA_ERR_INVALID_ARG", "LBSA_ERR_UNSUPPORTED", "LBSA_ERR_CUDA", "LBSA_ERR_OOM",
     "LBSA_ERR_BAD_INDEX", "LBSA_ERR_INVALID_SCORES", "LBSA_ERR_TIMEOUT",
@@ -96,6 +97,7 @@ def load_library():
         "lbsa_select_rule": (ctypes.c_int, [P, I32, I32, I32, I32, I32, I32, D, I32, ctypes.POINTER(P), P]),
         "lbsa_score_attend": (ctypes.c_int, [P, P, P, ctypes.POINTER(_Desc), I32, P, P, P, P]),
         "lbsa_attend": (ctypes.c_int, [P, P, P, ctypes.POINTER(_Desc), P, P, P, P]),
+        "lbsa_attend_backward": (ctypes.c_int, [P, P, P, P, P, P, ctypes.POINTER(_Desc), P, P, P, P, P]),
         "lbsa_free": (None, [P]),
         "lbsa_blockset_info": (ctypes.c_int, [P] + [ctypes.POINTER(I32)] * 5),
         "lbsa_blockset_views": (ctypes.c_int, [P, ctypes.POINTER(P), ctypes.POINTER(P)]),
@@ -365,6 +367,26 @@ def lbsa_attend(q, k, v, bs: Blockset, out=None, lse=None, want_lse=False, strea
     _check(load_library().lbsa_attend(_ptr(q), _ptr(k), _ptr(v), ctypes.byref(desc), bs.handle,
                                       _ptr(out), _ptr(lse), _stream(stream)))
     return (out, lse) if (want_lse or lse is not None) else out
+
+
+def lbsa_attend_backward(q, k, v, bs: Blockset, out, lse, dout, dq=None, dk=None, dv=None, stream=None):
+    """Gradients (dq, dk, dv) of lbsa_attend over bs, from its out and lse
+    (want_lse=True) and the gradient dout of out.  All tensors share q's shape,
+    strides and dtype.  The same inputs give the same bits on every call."""
+    for t in (k, v, out, dout):
+        _same_layout(q, t)
+    grads = [torch.empty_like(q) if t is None else t for t in (dq, dk, dv)]
+    for t in grads:
+        _same_layout(q, t)
+    desc = _desc(q)
+    B, H, N, _ = q.shape
+    if lse is None:
+        raise LbsaError(LBSA_ERR_INVALID_ARG, "lse is needed (lbsa_attend with want_lse=True)")
+    _on_device(lse, "lse", torch.float32, B * H * N)
+    _check(load_library().lbsa_attend_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse),
+                                               ctypes.byref(desc), bs.handle, *(_ptr(t) for t in grads),
+                                               _stream(stream)))
+    return tuple(grads)
 
 
 def lbsa_free(bs: Blockset):

@@ -1,0 +1,322 @@
+// Gradients of block-sparse attention: the per-call tables both kernels read,
+// and the fp32 kernel on CUDA cores.
+//
+// Mathematics.  For a query row r with kept keys K_r and the forward's lse_r:
+//   P_rc = exp(q_r . k_c / sqrt(d) - lse_r) on kept pairs, else 0
+//   D_r  = sum_e dout_re out_re             (= sum_c P_rc dP_rc)
+//   dP_rc = dout_r . v_c,   dS_rc = P_rc (dP_rc - D_r)
+//   dv_c = sum_r P_rc dout_r,  dk_c = sum_r dS_rc q_r / sqrt(d),
+//   dq_r = sum_c dS_rc k_c / sqrt(d)
+// dv and dk sum over the query blocks that keep a key block, dq over the key
+// blocks that a query block keeps.  Each of the two sums is walked by the CTAs
+// that own its rows, which compute S and dP twice over but need no atomics, no
+// fp32 gradient buffer in memory and no order between CTAs: the same inputs
+// give the same bits.
+//
+// Tables (scratch of the call): lse in log2 units and D, padded to whole
+// 128-row tiles (a row that keeps nothing, or does not exist, gets lse = +inf
+// and D = 0, so that its P is 0 without a test), and the kept pairs as bits in
+// both directions; the per-token sets go to [key block][query block].
+#include "lbsa_device.cuh"
+
+namespace lbsa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kPrepThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float2 load2(const T* p);
+template <>
+__device__ __forceinline__ float2 load2<float>(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
+template <>
+__device__ __forceinline__ float2 load2<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Blocks [0, index_blocks): 32 query blocks of one (batch, head) each, whose
+// lists become bit rows and, transposed in shared memory, one word of every
+// key block's bits.  The others: one warp a query row, D = dout . out.
+template <typename T, int D>
+__global__ void __launch_bounds__(kPrepThreads)
+attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, const float* __restrict__ lse,
+                        AttendGradArgs a, int index_blocks) {
+  extern __shared__ uint32_t bm[];                     // [32][W]
+  const int W = (a.nB + 31) >> 5;
+  if (blockIdx.x < index_blocks) {
+    const int w = blockIdx.x % W;
+    const long long bh = blockIdx.x / W;
+    for (int i = threadIdx.x; i < 32 * W; i += kPrepThreads) bm[i] = 0u;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = warp; r < 32; r += kPrepThreads / 32) {
+      const int i = w * 32 + r;
+      if (i >= a.nB) break;
+      const long long row = bh * a.nB + i;
+      const int cnt = a.counts[row];
+      for (int t = lane; t < cnt; t += 32) {
+        const int j = a.cols[row * a.nB + t];
+        if (j < 0 || j >= a.nB) {
+          raise_status(a.status, LBSA_ERR_BAD_INDEX);
+          continue;
+        }
+        atomicOr(&bm[r * W + (j >> 5)], 1u << (j & 31));
+        if (a.masks) a.masks_t[(bh * a.nB + j) * a.nB + i] = a.masks[row * a.nB + t];
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * W; i += kPrepThreads) {
+      const int r = i / W, q = w * 32 + r;
+      if (q < a.nB) a.bits[(bh * a.nB + q) * W + i - r * W] = bm[i];
+    }
+    for (int j = threadIdx.x; j < a.nB; j += kPrepThreads) {
+      uint32_t v = 0u;
+#pragma unroll
+      for (int r = 0; r < 32; ++r) v |= ((bm[r * W + (j >> 5)] >> (j & 31)) & 1u) << r;
+      a.bits_t[(bh * a.nB + j) * W + w] = v;
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x - index_blocks) * (kPrepThreads / 32) + (threadIdx.x >> 5);
+  const long long bh = row / a.Npad;
+  const int n = static_cast<int>(row - bh * a.Npad);
+  if (bh >= static_cast<long long>(a.B) * a.H) return;
+  float sum = 0.f, l = -INFINITY;
+  if (n < a.N_valid) {
+    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<long long>(b) * a.H);
+    const long long at = b * a.stride_b + h * a.stride_h + n * a.stride_n;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) {
+      const float2 x = load2<T>(out + at + e * 64 + lane * 2), y = load2<T>(dout + at + e * 64 + lane * 2);
+      sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = __ldg(lse + bh * a.N_valid + n);
+  }
+  if (lane == 0) {
+    const bool none = l == -INFINITY;
+    a.lse2[row] = none ? INFINITY : l * kLog2e;
+    a.delta[row] = none ? 0.f : sum;
+  }
+}
+
+// ------------------------------------------------------------------ CUDA cores
+// A CTA owns 64 rows (keys, or queries) and walks the 64-row pieces of the
+// other side that its block is kept with.  256 threads as 16 x 16: thread
+// (ty, tx) computes S and dP for rows ty + 16 i and columns tx + 16 j, then,
+// P and dS in shared memory, its 4 rows x d / 16 columns of the sums.
+constexpr int kPitch = 68;        // floats a row of P and dS: 16-byte rows, no bank conflicts
+
+template <typename T, int D>
+__device__ __forceinline__ void load_piece(float* s, const T* g, long long stride, int r0, int N) {
+  for (int i = threadIdx.x; i < 64 * D / 2; i += 256) {
+    const int r = i / (D / 2), e = (i - r * (D / 2)) * 2;
+    float2 v = make_float2(0.f, 0.f);
+    if (r0 + r < N) v = load2<T>(g + (r0 + r) * stride + e);
+    *reinterpret_cast<float2*>(s + r * (D + 4) + e) = v;
+  }
+}
+
+// acc[i][j] = row ty + 16 i of x  .  row tx + 16 j of y
+template <int D>
+__device__ __forceinline__ void dots(float (&acc)[4][4], const float* x, const float* y, int ty, int tx) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+  for (int e = 0; e < D; e += 4) {
+    float4 xr[4], yr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      xr[i] = *reinterpret_cast<const float4*>(x + (ty + 16 * i) * (D + 4) + e);
+      yr[i] = *reinterpret_cast<const float4*>(y + (tx + 16 * i) * (D + 4) + e);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = fmaf(xr[i].x, yr[j].x, fmaf(xr[i].y, yr[j].y, fmaf(xr[i].z, yr[j].z, fmaf(xr[i].w, yr[j].w, acc[i][j]))));
+  }
+}
+
+// acc[i][.] += sum_c w[ty + 16 i][c] y[c][columns of tx]
+template <int D>
+__device__ __forceinline__ void weighted(float (&acc)[4][D / 16], const float* w, const float* y, int ty, int tx) {
+#pragma unroll 2
+  for (int c = 0; c < 64; c += 4) {
+    float4 wr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wr[i] = *reinterpret_cast<const float4*>(w + (ty + 16 * i) * kPitch + c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int g = 0; g < D / 64; ++g) {
+        const float4 v = *reinterpret_cast<const float4*>(y + (c + k) * (D + 4) + g * 64 + tx * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = k == 0 ? wr[i].x : k == 1 ? wr[i].y : k == 2 ? wr[i].z : wr[i].w;
+          acc[i][g * 4 + 0] = fmaf(p, v.x, acc[i][g * 4 + 0]);
+          acc[i][g * 4 + 1] = fmaf(p, v.y, acc[i][g * 4 + 1]);
+          acc[i][g * 4 + 2] = fmaf(p, v.z, acc[i][g * 4 + 2]);
+          acc[i][g * 4 + 3] = fmaf(p, v.w, acc[i][g * 4 + 3]);
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void store_rows(T* g, long long stride, int r0, int N, const float (&acc)[4][D / 16], float f,
+                                           int ty, int tx) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + ty + 16 * i;
+    if (r >= N) continue;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      store4(g + r * stride + c * 64 + tx * 4, acc[i][c * 4] * f, acc[i][c * 4 + 1] * f, acc[i][c * 4 + 2] * f,
+             acc[i][c * 4 + 3] * f);
+  }
+}
+
+// blockIdx.x: pieces of keys (dk, dv), then pieces of queries (dq).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attend_grad_simt_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                              const T* __restrict__ v, const T* __restrict__ dout,
+                                                              AttendGradArgs a, int pieces) {
+  extern __shared__ float sm[];
+  constexpr int PIECE = 64 * (D + 4);
+  float *r1 = sm, *r2 = r1 + PIECE, *c1 = r2 + PIECE, *c2 = c1 + PIECE, *sp = c2 + PIECE, *sd = sp + 64 * kPitch;
+  const bool keys = blockIdx.x < pieces;
+  const int piece = keys ? blockIdx.x : blockIdx.x - pieces;
+  const int h = blockIdx.y, b = blockIdx.z, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int N = a.N_valid, shift = a.block == 128 ? 1 : 0, W = (a.nB + 31) >> 5;
+  const long long bh = static_cast<long long>(b) * a.H + h;
+  const long long base = b * a.stride_b + h * a.stride_h;
+  const int r0 = piece * 64, mine = piece >> shift;
+  const float scale = 1.0f / sqrtf(static_cast<float>(D)), scale2 = scale * kLog2e;
+  load_piece<T, D>(r1, (keys ? k : q) + base, a.stride_n, r0, N);
+  load_piece<T, D>(r2, (keys ? v : dout) + base, a.stride_n, r0, N);
+  float acc1[4][D / 16], acc2[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) acc1[i][j] = acc2[i][j] = 0.f;
+  const uint32_t* list = (keys ? a.bits_t : a.bits) + (bh * a.nB + mine) * W;
+  for (int w = 0; w < W; ++w) {
+    for (uint32_t word = __ldg(list + w); word; word &= word - 1) {
+      const int other = w * 32 + __ffs(word) - 1;
+      uint64_t set = ~0ull;       // per-token lists: the query tokens that keep the key block
+      if (a.masks) set = a.masks_t[(bh * a.nB + (keys ? mine : other)) * a.nB + (keys ? other : mine)];
+      for (int s = 0; s <= shift; ++s) {
+        const int c0 = (other << shift) * 64 + s * 64;
+        if (c0 >= N) break;
+        __syncthreads();          // the last piece's sums are done with c1, c2, sp, sd
+        load_piece<T, D>(c1, (keys ? q : k) + base, a.stride_n, c0, N);
+        load_piece<T, D>(c2, (keys ? dout : v) + base, a.stride_n, c0, N);
+        __syncthreads();
+        float p[4][4], g[4][4];
+        dots<D>(p, r1, c1, ty, tx);
+        dots<D>(g, r2, c2, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = ty + 16 * i, col = tx + 16 * j;
+            const int qi = keys ? col : row, ki = keys ? row : col;              // within their pieces
+            const int qn = (keys ? c0 : r0) + qi, kn = (keys ? r0 : c0) + ki;
+            const bool on = kn < N && ((set >> qi) & 1ull);
+            const float pr = on ? exp2f(fmaf(p[i][j], scale2, -a.lse2[bh * a.Npad + qn])) : 0.f;
+            sp[row * kPitch + col] = pr;
+            sd[row * kPitch + col] = on ? pr * (g[i][j] - a.delta[bh * a.Npad + qn]) : 0.f;
+          }
+        __syncthreads();
+        weighted<D>(acc1, sd, c1, ty, tx);
+        if (keys) weighted<D>(acc2, sp, c2, ty, tx);
+      }
+    }
+  }
+  if (keys) {
+    store_rows<T, D>(static_cast<T*>(a.dk) + base, a.stride_n, r0, N, acc1, scale, ty, tx);
+    store_rows<T, D>(static_cast<T*>(a.dv) + base, a.stride_n, r0, N, acc2, 1.f, ty, tx);
+  } else {
+    store_rows<T, D>(static_cast<T*>(a.dq) + base, a.stride_n, r0, N, acc1, scale, ty, tx);
+  }
+}
+
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+template <typename T, int D>
+cudaError_t prep(const void* out, const void* dout, const float* lse, const AttendGradArgs& a, cudaStream_t s) {
+  const long long W = (a.nB + 31) / 32, bh = static_cast<long long>(a.B) * a.H;
+  const long long index_blocks = bh * W, row_blocks = bh * a.Npad / (kPrepThreads / 32);
+  if (index_blocks + row_blocks > 2147483647ll) return cudaErrorInvalidValue;
+  attend_grad_prep_kernel<T, D><<<static_cast<unsigned>(index_blocks + row_blocks), kPrepThreads, 32 * W * 4, s>>>(
+      static_cast<const T*>(out), static_cast<const T*>(dout), lse, a, static_cast<int>(index_blocks));
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t simt(const void* q, const void* k, const void* v, const void* dout, const AttendGradArgs& a, cudaStream_t s) {
+  constexpr int smem = (4 * 64 * (D + 4) + 2 * 64 * kPitch) * 4;
+  cudaError_t e = cudaFuncSetAttribute(attend_grad_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int pieces = (a.N_valid + 63) / 64;
+  attend_grad_simt_kernel<T, D><<<dim3(2 * pieces, a.H, a.B), 256, smem, s>>>(
+      static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), static_cast<const T*>(dout), a, pieces);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attend_grad_workspace(AttendGradArgs* a, void* base) {
+  const size_t bh = static_cast<size_t>(a->B) * a->H, W = (a->nB + 31) / 32;
+  a->Npad = (a->N_valid + 127) / 128 * 128;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round256(bytes);
+    return static_cast<char*>(base) + here;
+  };
+  char* p[5];
+  p[0] = take(bh * a->Npad * sizeof(float));
+  p[1] = take(bh * a->Npad * sizeof(float));
+  p[2] = take(bh * a->nB * W * sizeof(uint32_t));
+  p[3] = take(bh * a->nB * W * sizeof(uint32_t));
+  p[4] = a->masks ? take(bh * a->nB * a->nB * sizeof(uint64_t)) : nullptr;
+  if (base) {
+    a->lse2 = reinterpret_cast<float*>(p[0]);
+    a->delta = reinterpret_cast<float*>(p[1]);
+    a->bits = reinterpret_cast<uint32_t*>(p[2]);
+    a->bits_t = reinterpret_cast<uint32_t*>(p[3]);
+    a->masks_t = reinterpret_cast<uint64_t*>(p[4]);
+  }
+  return at;
+}
+
+cudaError_t launch_attend_grad_prep(const void* out, const void* dout, const float* lse, int dtype,
+                                    const AttendGradArgs& a, cudaStream_t s) {
+  if (dtype == LBSA_BF16)
+    return a.d == 128 ? prep<__nv_bfloat16, 128>(out, dout, lse, a, s) : prep<__nv_bfloat16, 64>(out, dout, lse, a, s);
+  return a.d == 128 ? prep<float, 128>(out, dout, lse, a, s) : prep<float, 64>(out, dout, lse, a, s);
+}
+
+cudaError_t launch_attend_grad_simt(const void* q, const void* k, const void* v, const void* dout, int dtype,
+                                    const AttendGradArgs& a, cudaStream_t s) {
+  if (dtype == LBSA_BF16)
+    return a.d == 128 ? simt<__nv_bfloat16, 128>(q, k, v, dout, a, s) : simt<__nv_bfloat16, 64>(q, k, v, dout, a, s);
+  return a.d == 128 ? simt<float, 128>(q, k, v, dout, a, s) : simt<float, 64>(q, k, v, dout, a, s);
+}
+
+}  // namespace lbsa

@@ -636,6 +636,48 @@ int lbsa_attend(const void* q, const void* k, const void* v, const lbsa_qkv_desc
   return LBSA_OK;
 }
 
+int lbsa_attend_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                         const float* lse, const lbsa_qkv_desc* desc, const lbsa_blockset* bs, void* dq, void* dk,
+                         void* dv, void* stream) {
+  int rc;
+  if (desc)
+    log_line("lbsa_attend_backward B=%d H=%d N=%d d=%d dtype=%d blockset=%p (scope %d)", desc->B, desc->H, desc->N_valid,
+             desc->d, desc->dtype, static_cast<const void*>(bs), bs ? bs->scope : -1);
+  if ((rc = validate_desc(desc)) != LBSA_OK) return rc;
+  const void* ins[5] = {q, k, v, out, dout};
+  void* outs[3] = {dq, dk, dv};
+  static const char* names[8] = {"q", "k", "v", "out", "dout", "dq", "dk", "dv"};
+  for (int i = 0; i < 8; ++i)
+    if ((rc = validate_ptr(i < 5 ? ins[i] : outs[i - 5], names[i])) != LBSA_OK) return rc;
+  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(LBSA_ERR_INVALID_ARG, "lse is NULL or not 4-byte aligned");
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 5; ++j)
+      if (outs[i] == ins[j]) return fail(LBSA_ERR_INVALID_ARG, "%s may not alias %s", names[5 + i], names[j]);
+    if (outs[i] == outs[(i + 1) % 3]) return fail(LBSA_ERR_INVALID_ARG, "dq, dk and dv may not alias");
+  }
+  if (!bs) return fail(LBSA_ERR_INVALID_ARG, "blockset is NULL");
+  if (bs->B != desc->B || bs->H != desc->H || bs->nB != n_blocks(desc->N_valid, bs->block))
+    return fail(LBSA_ERR_INVALID_ARG, "blockset (B=%d, H=%d, nB=%d, block=%d) does not match q (B=%d, H=%d, N=%d)",
+                bs->B, bs->H, bs->nB, bs->block, desc->B, desc->H, desc->N_valid);
+  if (desc->B > 65535 || desc->H > 65535) return fail(LBSA_ERR_UNSUPPORTED, "B or H exceeds 65535");
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev != bs->device) return fail(LBSA_ERR_INVALID_ARG, "blockset lives on device %d, current is %d", bs->device, dev);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  lbsa::AttendGradArgs a{desc->B, desc->H, desc->N_valid, desc->d, bs->block, bs->nB, bs->counts, bs->cols, bs->masks,
+                         bs->status, dq, dk, dv, desc->stride_b, desc->stride_h, desc->stride_n, wait_limit()};
+  DeviceState* ds = nullptr;
+  Scratch ws;
+  if ((rc = device_state(&ds)) != LBSA_OK) return rc;
+  if ((rc = scratch_alloc(ds, lbsa::attend_grad_workspace(&a, nullptr), s, &ws)) != LBSA_OK) return rc;
+  lbsa::attend_grad_workspace(&a, ws.ptr);
+  cudaError_t e = lbsa::launch_attend_grad_prep(out, dout, lse, desc->dtype, a, s);
+  if (e == cudaSuccess) e = lbsa::launch_attend_grad_simt(q, k, v, dout, desc->dtype, a, s);
+  if (e != cudaSuccess) return cuda_fail(e, "lbsa_attend_backward launch");
+  return LBSA_OK;
+}
+
 void lbsa_free(lbsa_blockset* bs) {
   if (!bs) return;
   if (bs->base) cudaFreeAsync(bs->base, bs->stream);

@@ -145,6 +145,31 @@ cudaError_t launch_partition_perm(int T, int Hg, int Wg, int kind, int tt, int t
 cudaError_t launch_permute(const void* const* xs, void* const* ys, int count, const int32_t* perm,
                            const lbsa_qkv_desc& d, int inverse, int32_t* status, cudaStream_t s);
 
+// gradients of block-sparse attention (attend_grad.cu); strides in elements, shared by all tensors
+struct AttendGradArgs {
+  int B, H, N_valid, d, block, nB;
+  const int32_t* counts;
+  const int32_t* cols;
+  const uint64_t* masks;        // per-token scope, as AttendArgs::masks
+  int32_t* status;
+  void *dq, *dk, *dv;
+  int64_t stride_b, stride_h, stride_n;
+  long long wait_limit;
+  // the call's tables (attend_grad_workspace)
+  int Npad;                     // N_valid rounded up to whole 128-row tiles
+  float* lse2;                  // [B*H][Npad] lse in log2 units; +inf: the row keeps nothing
+  float* delta;                 // [B*H][Npad] sum of dout * out
+  uint32_t* bits;               // [B*H][nB queries][ceil(nB / 32)] kept key blocks
+  uint32_t* bits_t;             // [B*H][nB keys][ceil(nB / 32)] query blocks that keep it
+  uint64_t* masks_t;            // [B*H][nB keys][nB queries], written where bits are set
+};
+// sets Npad and, with base, the table pointers; returns the bytes wanted
+size_t attend_grad_workspace(AttendGradArgs* a, void* base);
+cudaError_t launch_attend_grad_prep(const void* out, const void* dout, const float* lse, int dtype,
+                                    const AttendGradArgs& a, cudaStream_t s);
+cudaError_t launch_attend_grad_simt(const void* q, const void* k, const void* v, const void* dout, int dtype,
+                                    const AttendGradArgs& a, cudaStream_t s);
+
 // rotary positions and the per-head norm (rope.cu); strides are in elements: batch, head, row
 struct RopeItem {
   const void* x;

@@ -258,6 +258,27 @@ int lbsa_select_routed(const float* scores, int32_t B, int32_t H, int32_t nB, in
 int lbsa_attend(const void* q, const void* k, const void* v, const lbsa_qkv_desc* desc,
                 const lbsa_blockset* bs, void* out, float* lse, void* stream);
 
+/* Gradients of lbsa_attend over the same blockset (training through frozen or
+ * freshly selected blocks; the selection itself has no gradient).
+ *   q, k, v    as given to lbsa_attend
+ *   out, lse   what it returned (lse is needed: fp32 [B, H, N_valid])
+ *   dout       gradient of out
+ *   dq, dk, dv out: gradients, dtype and strides of q; may alias nothing
+ * All of q, k, v, out, dout, dq, dk, dv share desc.  With P the probabilities
+ * of the kept pairs, D_r = sum_e dout_re out_re and dS = P (dout v^T - D):
+ * dv = P^T dout, dq = dS k / sqrt(d), dk = dS^T q / sqrt(d).  A row that keeps
+ * nothing (lse = -inf) gives and gets no gradient; a key block that no query
+ * keeps gets 0.  bf16: products on bf16 operands (P and dS rounded once), sums
+ * in fp32.  The sums are taken in a fixed order: the same inputs give the same
+ * bits.  Rows past N_valid are never read and never written.  A non-finite key
+ * or value in a block that a row does not keep can reach that row when the
+ * other 64-row half of its 128-row tile keeps the block, as in lbsa_attend.
+ * Scratch: 8 bytes a padded row, two bits a block pair, for per-token
+ * blocksets 8 bytes a block pair, from the library pool. */
+int lbsa_attend_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                         const float* lse, const lbsa_qkv_desc* desc, const lbsa_blockset* bs, void* dq, void* dk,
+                         void* dv, void* stream);
+
 /* Release a blockset (stream-ordered on the stream it was created on).  NULL is a no-op. */
 void lbsa_free(lbsa_blockset* bs);
 
