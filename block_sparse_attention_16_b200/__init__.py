@@ -97,7 +97,8 @@ def load_library():
         "lbsa_select_rule": (ctypes.c_int, [P, I32, I32, I32, I32, I32, I32, D, I32, ctypes.POINTER(P), P]),
         "lbsa_score_attend": (ctypes.c_int, [P, P, P, ctypes.POINTER(_Desc), I32, P, P, P, P]),
         "lbsa_attend": (ctypes.c_int, [P, P, P, ctypes.POINTER(_Desc), P, P, P, P]),
-        "lbsa_attend_backward": (ctypes.c_int, [P, P, P, P, P, P, ctypes.POINTER(_Desc), P, P, P, P, P]),
+        "lbsa_attend_backward": (ctypes.c_int, [P, P, P, P, P, P, ctypes.POINTER(_Desc), ctypes.POINTER(I64),
+                                                P, P, P, P, P]),
         "lbsa_free": (None, [P]),
         "lbsa_blockset_info": (ctypes.c_int, [P] + [ctypes.POINTER(I32)] * 5),
         "lbsa_blockset_views": (ctypes.c_int, [P, ctypes.POINTER(P), ctypes.POINTER(P)]),
@@ -371,22 +372,28 @@ def lbsa_attend(q, k, v, bs: Blockset, out=None, lse=None, want_lse=False, strea
 
 def lbsa_attend_backward(q, k, v, bs: Blockset, out, lse, dout, dq=None, dk=None, dv=None, stream=None):
     """Gradients (dq, dk, dv) of lbsa_attend over bs, from its out and lse
-    (want_lse=True) and the gradient dout of out.  All tensors share q's shape,
-    strides and dtype.  The same inputs give the same bits on every call."""
-    for t in (k, v, out, dout):
-        _same_layout(q, t)
-    grads = [torch.empty_like(q) if t is None else t for t in (dq, dk, dv)]
-    for t in grads:
-        _same_layout(q, t)
+    (want_lse=True) and the gradient dout of out.  The tensors share q's shape
+    and dtype, their strides may differ (new gradients take those of q, k and
+    v).  The same inputs give the same bits on every call."""
     desc = _desc(q)
+    dq, dk, dv = (torch.empty_like(x) if t is None else t for x, t in ((q, dq), (k, dk), (v, dv)))
+    tensors = (q, k, v, out, dout, dq, dk, dv)
+    strides = (ctypes.c_int64 * 24)()
+    for i, t in enumerate(tensors):
+        if t.shape != q.shape or t.dtype != q.dtype or t.device != q.device or t.stride(3) != 1:
+            raise LbsaError(LBSA_ERR_INVALID_ARG, "q, k, v, out, dout and the gradients must share shape, dtype and "
+                                                  "device, with a contiguous last dim")
+        for j, (st, size) in enumerate(zip(t.stride()[:3], t.shape)):
+            strides[3 * i + j] = st if size > 1 else q.shape[3]
     B, H, N, _ = q.shape
     if lse is None:
         raise LbsaError(LBSA_ERR_INVALID_ARG, "lse is needed (lbsa_attend with want_lse=True)")
     _on_device(lse, "lse", torch.float32, B * H * N)
+    desc.stride_b, desc.stride_h, desc.stride_n = strides[0:3]
     _check(load_library().lbsa_attend_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse),
-                                               ctypes.byref(desc), bs.handle, *(_ptr(t) for t in grads),
+                                               ctypes.byref(desc), strides, bs.handle, _ptr(dq), _ptr(dk), _ptr(dv),
                                                _stream(stream)))
-    return tuple(grads)
+    return dq, dk, dv
 
 
 def lbsa_free(bs: Blockset):

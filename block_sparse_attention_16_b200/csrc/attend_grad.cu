@@ -25,6 +25,10 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPrepThreads = 256;
 
+__device__ __forceinline__ long long offset(const GradStride& s, int b, int h, int n) {
+  return b * s.b + h * s.h + n * s.n;
+}
+
 template <typename T>
 __device__ __forceinline__ float2 load2(const T* p);
 template <>
@@ -86,10 +90,11 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
   float sum = 0.f, l = -INFINITY;
   if (n < a.N_valid) {
     const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<long long>(b) * a.H);
-    const long long at = b * a.stride_b + h * a.stride_h + n * a.stride_n;
+    const T* po = out + offset(a.st[kOut], b, h, n) + lane * 2;
+    const T* pd = dout + offset(a.st[kDout], b, h, n) + lane * 2;
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) {
-      const float2 x = load2<T>(out + at + e * 64 + lane * 2), y = load2<T>(dout + at + e * 64 + lane * 2);
+      const float2 x = load2<T>(po + e * 64), y = load2<T>(pd + e * 64);
       sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
     }
 #pragma unroll
@@ -203,11 +208,14 @@ __global__ void __launch_bounds__(256) attend_grad_simt_kernel(const T* __restri
   const int h = blockIdx.y, b = blockIdx.z, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int N = a.N_valid, shift = a.block == 128 ? 1 : 0, W = (a.nB + 31) >> 5;
   const long long bh = static_cast<long long>(b) * a.H + h;
-  const long long base = b * a.stride_b + h * a.stride_h;
+  const GradStride &s_r1 = a.st[keys ? kK : kQ], &s_r2 = a.st[keys ? kV : kDout];
+  const GradStride &s_c1 = a.st[keys ? kQ : kK], &s_c2 = a.st[keys ? kDout : kV];
+  const T* g1 = (keys ? q : k) + offset(s_c1, b, h, 0);
+  const T* g2 = (keys ? dout : v) + offset(s_c2, b, h, 0);
   const int r0 = piece * 64, mine = piece >> shift;
   const float scale = 1.0f / sqrtf(static_cast<float>(D)), scale2 = scale * kLog2e;
-  load_piece<T, D>(r1, (keys ? k : q) + base, a.stride_n, r0, N);
-  load_piece<T, D>(r2, (keys ? v : dout) + base, a.stride_n, r0, N);
+  load_piece<T, D>(r1, (keys ? k : q) + offset(s_r1, b, h, 0), s_r1.n, r0, N);
+  load_piece<T, D>(r2, (keys ? v : dout) + offset(s_r2, b, h, 0), s_r2.n, r0, N);
   float acc1[4][D / 16], acc2[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -223,8 +231,8 @@ __global__ void __launch_bounds__(256) attend_grad_simt_kernel(const T* __restri
         const int c0 = (other << shift) * 64 + s * 64;
         if (c0 >= N) break;
         __syncthreads();          // the last piece's sums are done with c1, c2, sp, sd
-        load_piece<T, D>(c1, (keys ? q : k) + base, a.stride_n, c0, N);
-        load_piece<T, D>(c2, (keys ? dout : v) + base, a.stride_n, c0, N);
+        load_piece<T, D>(c1, g1, s_c1.n, c0, N);
+        load_piece<T, D>(c2, g2, s_c2.n, c0, N);
         __syncthreads();
         float p[4][4], g[4][4];
         dots<D>(p, r1, c1, ty, tx);
@@ -248,10 +256,10 @@ __global__ void __launch_bounds__(256) attend_grad_simt_kernel(const T* __restri
     }
   }
   if (keys) {
-    store_rows<T, D>(static_cast<T*>(a.dk) + base, a.stride_n, r0, N, acc1, scale, ty, tx);
-    store_rows<T, D>(static_cast<T*>(a.dv) + base, a.stride_n, r0, N, acc2, 1.f, ty, tx);
+    store_rows<T, D>(static_cast<T*>(a.dk) + offset(a.st[kDk], b, h, 0), a.st[kDk].n, r0, N, acc1, scale, ty, tx);
+    store_rows<T, D>(static_cast<T*>(a.dv) + offset(a.st[kDv], b, h, 0), a.st[kDv].n, r0, N, acc2, 1.f, ty, tx);
   } else {
-    store_rows<T, D>(static_cast<T*>(a.dq) + base, a.stride_n, r0, N, acc1, scale, ty, tx);
+    store_rows<T, D>(static_cast<T*>(a.dq) + offset(a.st[kDq], b, h, 0), a.st[kDq].n, r0, N, acc1, scale, ty, tx);
   }
 }
 

@@ -637,8 +637,8 @@ int lbsa_attend(const void* q, const void* k, const void* v, const lbsa_qkv_desc
 }
 
 int lbsa_attend_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
-                         const float* lse, const lbsa_qkv_desc* desc, const lbsa_blockset* bs, void* dq, void* dk,
-                         void* dv, void* stream) {
+                         const float* lse, const lbsa_qkv_desc* desc, const int64_t* strides,
+                         const lbsa_blockset* bs, void* dq, void* dk, void* dv, void* stream) {
   int rc;
   if (desc)
     log_line("lbsa_attend_backward B=%d H=%d N=%d d=%d dtype=%d blockset=%p (scope %d)", desc->B, desc->H, desc->N_valid,
@@ -649,6 +649,17 @@ int lbsa_attend_backward(const void* q, const void* k, const void* v, const void
   static const char* names[8] = {"q", "k", "v", "out", "dout", "dq", "dk", "dv"};
   for (int i = 0; i < 8; ++i)
     if ((rc = validate_ptr(i < 5 ? ins[i] : outs[i - 5], names[i])) != LBSA_OK) return rc;
+  lbsa::GradStride st[lbsa::kGradTensors];
+  for (int i = 0; i < lbsa::kGradTensors; ++i) {
+    lbsa_qkv_desc one = *desc;
+    if (strides) {
+      one.stride_b = strides[3 * i];
+      one.stride_h = strides[3 * i + 1];
+      one.stride_n = strides[3 * i + 2];
+      if ((rc = validate_desc(&one)) != LBSA_OK) return rc;
+    }
+    st[i] = lbsa::GradStride{one.stride_b, one.stride_h, one.stride_n};
+  }
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return fail(LBSA_ERR_INVALID_ARG, "lse is NULL or not 4-byte aligned");
   for (int i = 0; i < 3; ++i) {
@@ -666,7 +677,8 @@ int lbsa_attend_backward(const void* q, const void* k, const void* v, const void
   if (dev != bs->device) return fail(LBSA_ERR_INVALID_ARG, "blockset lives on device %d, current is %d", bs->device, dev);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   lbsa::AttendGradArgs a{desc->B, desc->H, desc->N_valid, desc->d, bs->block, bs->nB, bs->counts, bs->cols, bs->masks,
-                         bs->status, dq, dk, dv, desc->stride_b, desc->stride_h, desc->stride_n, wait_limit()};
+                         bs->status, dq, dk, dv, {}, wait_limit()};
+  for (int i = 0; i < lbsa::kGradTensors; ++i) a.st[i] = st[i];
   DeviceState* ds = nullptr;
   Scratch ws;
   if ((rc = device_state(&ds)) != LBSA_OK) return rc;

@@ -145,7 +145,11 @@ cudaError_t launch_partition_perm(int T, int Hg, int Wg, int kind, int tt, int t
 cudaError_t launch_permute(const void* const* xs, void* const* ys, int count, const int32_t* perm,
                            const lbsa_qkv_desc& d, int inverse, int32_t* status, cudaStream_t s);
 
-// gradients of block-sparse attention (attend_grad.cu); strides in elements, shared by all tensors
+// gradients of block-sparse attention (attend_grad.cu)
+enum GradTensor { kQ, kK, kV, kOut, kDout, kDq, kDk, kDv, kGradTensors };
+struct GradStride {
+  int64_t b, h, n;              // elements; the d stride is 1
+};
 struct AttendGradArgs {
   int B, H, N_valid, d, block, nB;
   const int32_t* counts;
@@ -153,7 +157,7 @@ struct AttendGradArgs {
   const uint64_t* masks;        // per-token scope, as AttendArgs::masks
   int32_t* status;
   void *dq, *dk, *dv;
-  int64_t stride_b, stride_h, stride_n;
+  GradStride st[kGradTensors];
   long long wait_limit;
   // the call's tables (attend_grad_workspace)
   int Npad;                     // N_valid rounded up to whole 128-row tiles

@@ -263,8 +263,11 @@ int lbsa_attend(const void* q, const void* k, const void* v, const lbsa_qkv_desc
  *   q, k, v    as given to lbsa_attend
  *   out, lse   what it returned (lse is needed: fp32 [B, H, N_valid])
  *   dout       gradient of out
- *   dq, dk, dv out: gradients, dtype and strides of q; may alias nothing
- * All of q, k, v, out, dout, dq, dk, dv share desc.  With P the probabilities
+ *   dq, dk, dv out: gradients, dtype of q; may alias nothing
+ *   strides    host [8][3]: element strides (batch, head, row) of q, k, v, out,
+ *              dout, dq, dk, dv in place of desc's (the gradient of a
+ *              layer's output seldom has q's), or NULL: all have desc's
+ * With P the probabilities
  * of the kept pairs, D_r = sum_e dout_re out_re and dS = P (dout v^T - D):
  * dv = P^T dout, dq = dS k / sqrt(d), dk = dS^T q / sqrt(d).  A row that keeps
  * nothing (lse = -inf) gives and gets no gradient; a key block that no query
@@ -276,8 +279,8 @@ int lbsa_attend(const void* q, const void* k, const void* v, const lbsa_qkv_desc
  * Scratch: 8 bytes a padded row, two bits a block pair, for per-token
  * blocksets 8 bytes a block pair, from the library pool. */
 int lbsa_attend_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
-                         const float* lse, const lbsa_qkv_desc* desc, const lbsa_blockset* bs, void* dq, void* dk,
-                         void* dv, void* stream);
+                         const float* lse, const lbsa_qkv_desc* desc, const int64_t* strides,
+                         const lbsa_blockset* bs, void* dq, void* dk, void* dv, void* stream);
 
 /* Release a blockset (stream-ordered on the stream it was created on).  NULL is a no-op. */
 void lbsa_free(lbsa_blockset* bs);

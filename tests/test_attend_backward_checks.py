@@ -10,14 +10,15 @@ INV, UNS = lbsa.LBSA_ERR_INVALID_ARG, lbsa.LBSA_ERR_UNSUPPORTED
 NAMES = ["q", "k", "v", "out", "dout", "lse", "dq", "dk", "dv"]
 
 
-def _call(desc=None, bs=None, **at):
+def _call(desc=None, bs=None, strides=None, **at):
     # addresses that are never dereferenced: validation fails first
     p = {n: 0x10000 * (i + 1) for i, n in enumerate(NAMES)}
     p.update(at)
     d = dict(B=1, H=2, N_valid=256, d=64, dtype=1, reserved=0, stride_b=2 * 256 * 64, stride_h=256 * 64, stride_n=64)
     d.update(desc or {})
     args = [ctypes.c_void_p(p[n]) for n in NAMES]
-    rc = lbsa.load_library().lbsa_attend_backward(*args[:6], ctypes.byref(lbsa._Desc(**d)), bs, *args[6:], None)
+    rc = lbsa.load_library().lbsa_attend_backward(*args[:6], ctypes.byref(lbsa._Desc(**d)),
+                                                  (ctypes.c_int64 * 24)(*strides) if strides else None, bs, *args[6:], None)
     assert rc == lbsa.LBSA_OK or lbsa.lbsa_last_error()
     return rc
 
@@ -26,6 +27,15 @@ def _call(desc=None, bs=None, **at):
                                        (dict(stride_n=60), INV), (dict(stride_n=65), INV), (dict(stride_h=0), INV)])
 def test_desc_is_checked(desc, code):
     assert _call(desc) == code
+
+
+@pytest.mark.parametrize("tensor", range(8))
+@pytest.mark.parametrize("at,value", [(0, 0), (1, -64), (2, 32), (2, 66)])
+def test_strides_are_checked(tensor, at, value):
+    strides = [2 * 256 * 64, 256 * 64, 64] * 8
+    strides[3 * tensor + at] = value
+    assert _call(strides=strides) == INV
+    assert "stride" in lbsa.lbsa_last_error()
 
 
 @pytest.mark.parametrize("name", NAMES)

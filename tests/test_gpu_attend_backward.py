@@ -156,6 +156,29 @@ def test_projection_strides(dtype):
 
 
 @BOTH
+def test_every_tensor_with_strides_of_its_own(dtype):
+    B, H, N, d, keep = 2, 3, 200, 64, _keep(8, 2, 3, 4, 4, 0.6)
+    q, k, v, dout = (_normal(60 + i, B, H, N, d, dtype=dtype) for i in range(4))
+    bs = _blockset(keep, 64)
+    out, lse = lbsa.lbsa_attend(q, k, v, bs, want_lse=True)
+    want = lbsa.lbsa_attend_backward(q, k, v, bs, out, lse, dout)
+
+    def other(x, i):                                      # rows apart, heads innermost, batches in a wider buffer
+        if i % 3 == 0:
+            return x.transpose(1, 2).contiguous().transpose(1, 2)
+        buf = torch.full((B, H + 1, N + i, d + 8 * i), float("nan"), dtype=x.dtype, device=x.device)
+        buf[:, :H, :N, :d] = x
+        return buf[:, :H, :N, :d]
+    ins = [other(x, i) for i, x in enumerate((q, k, v, out, dout))]
+    outs = [other(torch.zeros_like(q), i) for i in (4, 3, 2)]
+    lbsa.lbsa_attend_backward(*ins[:3], bs, ins[3], lse, ins[4], *outs)
+    for a, b in zip(outs, want):
+        assert torch.equal(a, b)
+    for a, b in zip(lbsa.lbsa_attend_backward(*ins[:3], bs, ins[3], lse, ins[4]), want):
+        assert torch.equal(a, b)
+
+
+@BOTH
 def test_rows_past_the_last_token_are_neither_read_nor_written(dtype):
     N, keep = 150, _keep(7, 1, 2, 3, 3, 0.7)
     bufs = [_normal(70 + i, 1, 2, 192, 64, dtype=dtype) for i in range(4)]
