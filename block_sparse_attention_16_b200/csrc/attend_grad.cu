@@ -115,12 +115,12 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
 // P and dS in shared memory, its 4 rows x d / 16 columns of the sums.
 constexpr int kPitch = 68;        // floats a row of P and dS: 16-byte rows, no bank conflicts
 
-template <typename T, int D>
-__device__ __forceinline__ void load_piece(float* s, const T* g, long long stride, int r0, int N) {
+template <int D>
+__device__ __forceinline__ void load_piece(float* s, const float* g, long long stride, int r0, int N) {
   for (int i = threadIdx.x; i < 64 * D / 2; i += 256) {
     const int r = i / (D / 2), e = (i - r * (D / 2)) * 2;
     float2 v = make_float2(0.f, 0.f);
-    if (r0 + r < N) v = load2<T>(g + (r0 + r) * stride + e);
+    if (r0 + r < N) v = load2<float>(g + (r0 + r) * stride + e);
     *reinterpret_cast<float2*>(s + r * (D + 4) + e) = v;
   }
 }
@@ -174,15 +174,8 @@ __device__ __forceinline__ void weighted(float (&acc)[4][D / 16], const float* w
   }
 }
 
-__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
-  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
-}
-
-template <typename T, int D>
-__device__ __forceinline__ void store_rows(T* g, long long stride, int r0, int N, const float (&acc)[4][D / 16], float f,
+template <int D>
+__device__ __forceinline__ void store_rows(float* g, long long stride, int r0, int N, const float (&acc)[4][D / 16], float f,
                                            int ty, int tx) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -190,16 +183,16 @@ __device__ __forceinline__ void store_rows(T* g, long long stride, int r0, int N
     if (r >= N) continue;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
-      store4(g + r * stride + c * 64 + tx * 4, acc[i][c * 4] * f, acc[i][c * 4 + 1] * f, acc[i][c * 4 + 2] * f,
-             acc[i][c * 4 + 3] * f);
+      *reinterpret_cast<float4*>(g + r * stride + c * 64 + tx * 4) =
+          make_float4(acc[i][c * 4] * f, acc[i][c * 4 + 1] * f, acc[i][c * 4 + 2] * f, acc[i][c * 4 + 3] * f);
   }
 }
 
 // blockIdx.x: pieces of keys (dk, dv), then pieces of queries (dq).
-template <typename T, int D>
-__global__ void __launch_bounds__(256) attend_grad_simt_kernel(const T* __restrict__ q, const T* __restrict__ k,
-                                                              const T* __restrict__ v, const T* __restrict__ dout,
-                                                              AttendGradArgs a, int pieces) {
+template <int D>
+__global__ void __launch_bounds__(256) attend_grad_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
+                                                             const float* __restrict__ v, const float* __restrict__ dout,
+                                                             AttendGradArgs a, int pieces) {
   extern __shared__ float sm[];
   constexpr int PIECE = 64 * (D + 4);
   float *r1 = sm, *r2 = r1 + PIECE, *c1 = r2 + PIECE, *c2 = c1 + PIECE, *sp = c2 + PIECE, *sd = sp + 64 * kPitch;
@@ -210,12 +203,12 @@ __global__ void __launch_bounds__(256) attend_grad_simt_kernel(const T* __restri
   const long long bh = static_cast<long long>(b) * a.H + h;
   const GradStride &s_r1 = a.st[keys ? kK : kQ], &s_r2 = a.st[keys ? kV : kDout];
   const GradStride &s_c1 = a.st[keys ? kQ : kK], &s_c2 = a.st[keys ? kDout : kV];
-  const T* g1 = (keys ? q : k) + offset(s_c1, b, h, 0);
-  const T* g2 = (keys ? dout : v) + offset(s_c2, b, h, 0);
+  const float* g1 = (keys ? q : k) + offset(s_c1, b, h, 0);
+  const float* g2 = (keys ? dout : v) + offset(s_c2, b, h, 0);
   const int r0 = piece * 64, mine = piece >> shift;
   const float scale = 1.0f / sqrtf(static_cast<float>(D)), scale2 = scale * kLog2e;
-  load_piece<T, D>(r1, (keys ? k : q) + offset(s_r1, b, h, 0), s_r1.n, r0, N);
-  load_piece<T, D>(r2, (keys ? v : dout) + offset(s_r2, b, h, 0), s_r2.n, r0, N);
+  load_piece<D>(r1, (keys ? k : q) + offset(s_r1, b, h, 0), s_r1.n, r0, N);
+  load_piece<D>(r2, (keys ? v : dout) + offset(s_r2, b, h, 0), s_r2.n, r0, N);
   float acc1[4][D / 16], acc2[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -231,8 +224,8 @@ __global__ void __launch_bounds__(256) attend_grad_simt_kernel(const T* __restri
         const int c0 = (other << shift) * 64 + s * 64;
         if (c0 >= N) break;
         __syncthreads();          // the last piece's sums are done with c1, c2, sp, sd
-        load_piece<T, D>(c1, g1, s_c1.n, c0, N);
-        load_piece<T, D>(c2, g2, s_c2.n, c0, N);
+        load_piece<D>(c1, g1, s_c1.n, c0, N);
+        load_piece<D>(c2, g2, s_c2.n, c0, N);
         __syncthreads();
         float p[4][4], g[4][4];
         dots<D>(p, r1, c1, ty, tx);
@@ -256,10 +249,10 @@ __global__ void __launch_bounds__(256) attend_grad_simt_kernel(const T* __restri
     }
   }
   if (keys) {
-    store_rows<T, D>(static_cast<T*>(a.dk) + offset(a.st[kDk], b, h, 0), a.st[kDk].n, r0, N, acc1, scale, ty, tx);
-    store_rows<T, D>(static_cast<T*>(a.dv) + offset(a.st[kDv], b, h, 0), a.st[kDv].n, r0, N, acc2, 1.f, ty, tx);
+    store_rows<D>(static_cast<float*>(a.dk) + offset(a.st[kDk], b, h, 0), a.st[kDk].n, r0, N, acc1, scale, ty, tx);
+    store_rows<D>(static_cast<float*>(a.dv) + offset(a.st[kDv], b, h, 0), a.st[kDv].n, r0, N, acc2, 1.f, ty, tx);
   } else {
-    store_rows<T, D>(static_cast<T*>(a.dq) + offset(a.st[kDq], b, h, 0), a.st[kDq].n, r0, N, acc1, scale, ty, tx);
+    store_rows<D>(static_cast<float*>(a.dq) + offset(a.st[kDq], b, h, 0), a.st[kDq].n, r0, N, acc1, scale, ty, tx);
   }
 }
 
@@ -275,14 +268,13 @@ cudaError_t prep(const void* out, const void* dout, const float* lse, const Atte
   return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t simt(const void* q, const void* k, const void* v, const void* dout, const AttendGradArgs& a, cudaStream_t s) {
+template <int D>
+cudaError_t f32(const float* q, const float* k, const float* v, const float* dout, const AttendGradArgs& a, cudaStream_t s) {
   constexpr int smem = (4 * 64 * (D + 4) + 2 * 64 * kPitch) * 4;
-  cudaError_t e = cudaFuncSetAttribute(attend_grad_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(attend_grad_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int pieces = (a.N_valid + 63) / 64;
-  attend_grad_simt_kernel<T, D><<<dim3(2 * pieces, a.H, a.B), 256, smem, s>>>(
-      static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), static_cast<const T*>(dout), a, pieces);
+  attend_grad_f32_kernel<D><<<dim3(2 * pieces, a.H, a.B), 256, smem, s>>>(q, k, v, dout, a, pieces);
   return cudaGetLastError();
 }
 
@@ -320,11 +312,9 @@ cudaError_t launch_attend_grad_prep(const void* out, const void* dout, const flo
   return a.d == 128 ? prep<float, 128>(out, dout, lse, a, s) : prep<float, 64>(out, dout, lse, a, s);
 }
 
-cudaError_t launch_attend_grad_simt(const void* q, const void* k, const void* v, const void* dout, int dtype,
-                                    const AttendGradArgs& a, cudaStream_t s) {
-  if (dtype == LBSA_BF16)
-    return a.d == 128 ? simt<__nv_bfloat16, 128>(q, k, v, dout, a, s) : simt<__nv_bfloat16, 64>(q, k, v, dout, a, s);
-  return a.d == 128 ? simt<float, 128>(q, k, v, dout, a, s) : simt<float, 64>(q, k, v, dout, a, s);
+cudaError_t launch_attend_grad_f32(const float* q, const float* k, const float* v, const float* dout,
+                                   const AttendGradArgs& a, cudaStream_t s) {
+  return a.d == 128 ? f32<128>(q, k, v, dout, a, s) : f32<64>(q, k, v, dout, a, s);
 }
 
 }  // namespace lbsa

@@ -1,0 +1,482 @@
+// Gradients of block-sparse attention on sm_100a tensor cores (bf16 in, fp32
+// accumulate).  The mathematics and the tables are attend_grad.cu's.
+//
+// Two kinds of CTA in one launch, each owning 128 rows and walking the union of
+// its two 64-row blocks' lists in steps of 128 columns (two 64-row pieces of
+// the other side, which need not be neighbours):
+//   keys      S^T = K Q^T, dP^T = V dO^T (rows are keys, columns queries), then
+//             dV += P^T dO and dK += dS^T Q: four products a step
+//   queries   S = Q K^T, dP = dO V^T, then dQ += dS K: three products a step
+// Seven products in place of the formula's five, for which no gradient is
+// added across CTAs: no atomics, no fp32 dQ in memory (a read-modify-write of
+// 64 KB a step) and the same bits on every call.
+//
+// Warp roles (320 threads, one CTA an SM):
+//   warps 0-3, 4-7  thread t owns row t % 128 = TMEM lane; the first four warps
+//             take a step's first piece (columns 0-63), the others the second.
+//             P = 2^(S scale - lse), packed to bf16 over the S columns just
+//             read (keys); dS = P (dP - D), over the dP columns (keys) or into
+//             one of two buffers (queries), and at the end the rows' sums.
+//   warp 8    TMA producer: walks the two bit rows, loads the CTA's own tiles
+//             once, then the first operand's pieces through a 3-stage and the
+//             second's (with lse and D of the columns) through a 2-stage ring.
+//   warp 9    UMMA issuer.
+// TMEM columns: [0,128) S, [128,256) dP, [256,256+D) dK or dQ, [384,384+D) dV,
+// or two dS buffers of 64 (queries).
+#include "lbsa_device.cuh"
+
+namespace lbsa {
+namespace {
+
+constexpr int BM = 128;             // rows of a tile, columns of a step
+constexpr int kThreads = 320;
+constexpr int N1 = 3, N2 = 2;       // ring depths of the two operands
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kS = 0, kDP = 128, kAcc1 = 256, kAcc2 = 384, kDS = 384;
+
+template <int D>
+struct Layout {
+  static constexpr int TILE = BM * D * 2;
+  static constexpr int OFF_R1 = 0, OFF_R2 = TILE;
+  static constexpr int OFF_C1 = 2 * TILE, OFF_C2 = OFF_C1 + N1 * TILE;
+  static constexpr int OFF_COL = OFF_C2 + N2 * TILE;         // per stage: 128 lse, 128 D
+  static constexpr int OFF_BAR = OFF_COL + N2 * 2 * BM * 4;
+  static constexpr int OFF_MISC = OFF_BAR + 16 * 8;          // tmem, abort, count, pad, entries[N2][2]
+  static constexpr int BYTES = OFF_MISC + 64;
+};
+
+struct Bars {
+  uint64_t *r_full, *c1_full, *c2_full, *c_empty, *s_full, *dp_full, *s_done, *dp_done, *ds_full, *drain;
+};
+__device__ __forceinline__ Bars make_bars(uint8_t* base) {
+  uint64_t* b = reinterpret_cast<uint64_t*>(base);
+  return Bars{b, b + 1, b + 4, b + 6, b + 8, b + 9, b + 10, b + 11, b + 12, b + 13};
+}
+
+// Bulk copy of `bytes` (a multiple of 16) into shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+struct Tile {
+  int tile, h, b, n_steps;
+  long long bh;
+};
+
+// The walk over a tile's kept pieces: the set bits of its two bit rows.
+struct Walk {
+  const uint32_t *r0, *r1;          // r1: NULL for 128-row blocks and a missing second block
+  int W, w, shift, sub;
+  uint32_t a, b, rest;              // words and their union's bits still to come
+  __device__ __forceinline__ void init(const uint32_t* x, const uint32_t* y, int words, int sh) {
+    r0 = x;
+    r1 = y;
+    W = words;
+    shift = sh;
+    w = -1;
+    sub = 0;
+    rest = 0u;
+  }
+  // the next piece (64-row index) | the halves of the tile that keep it << 30; 0xFFFFFFFF at the end
+  __device__ __forceinline__ uint32_t next() {
+    while (rest == 0u) {
+      if (++w >= W) return 0xFFFFFFFFu;
+      a = __ldg(r0 + w);
+      b = r1 ? __ldg(r1 + w) : (shift ? a : 0u);
+      rest = a | b;
+    }
+    const int bit = __ffs(rest) - 1;
+    const uint32_t halves = ((a >> bit) & 1u) | (((b >> bit) & 1u) << 1);
+    const uint32_t piece = ((static_cast<uint32_t>(w * 32 + bit)) << shift) + sub;
+    if (sub == shift) {
+      rest &= rest - 1u;
+      sub = 0;
+    } else {
+      sub = 1;
+    }
+    return piece | (halves << 30);
+  }
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long wl, int32_t* status,
+                                          volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wl, status, abort_flag));
+}
+// Every lane's TMEM accesses are done: one arrival for the warp.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+template <int D, bool KEYS>
+__device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const CUtensorMap* r1, const CUtensorMap* r2,
+                                        const CUtensorMap* c1, const CUtensorMap* c2, const AttendGradArgs& a,
+                                        const Tile& t, Walk walk, uint32_t* entries, volatile int* abort_flag) {
+  using L = Layout<D>;
+  auto load = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int half, int piece) {
+    for (int c = 0; c < D / 64; ++c) tma_load_4d(dst + c * BM * 128 + half * 64 * 128, m, bar, c * 64, piece * 64, t.h, t.b);
+  };
+  if (t.n_steps == 0) return;
+  mbar_arrive_expect_tx(bars.r_full, 2 * L::TILE);
+  for (int p = 0; p < 2; ++p) {
+    load(smem + L::OFF_R1, r1, bars.r_full, p, t.tile * 2 + p);
+    load(smem + L::OFF_R2, r2, bars.r_full, p, t.tile * 2 + p);
+  }
+  int j = 0, done1 = 0, done2 = 0;
+  for (; j < t.n_steps; ++j) {
+    uint32_t e[2];
+    e[0] = walk.next();
+    e[1] = walk.next();
+    if (e[1] == 0xFFFFFFFFu) e[1] = e[0] & 0x3FFFFFFFu;       // an odd tail: the piece again, kept by nobody
+    // stage j % 3 was freed by step j - 3, whose end was waited for below at step j - 1
+    uint8_t* s1 = smem + L::OFF_C1 + (j % N1) * L::TILE;
+    uint64_t* f1 = bars.c1_full + j % N1;
+    mbar_arrive_expect_tx(f1, L::TILE);
+    for (int p = 0; p < 2; ++p) load(s1, c1, f1, p, e[p] & 0x3FFFFFFFu);
+    done1 = j + 1;
+    if (j >= N2 && !mbar_wait(bars.c_empty + (j & 1), ((j >> 1) & 1) ^ 1, a.wait_limit, a.status, abort_flag)) break;
+    uint8_t* s2 = smem + L::OFF_C2 + (j & 1) * L::TILE;
+    uint64_t* f2 = bars.c2_full + (j & 1);
+    entries[(j & 1) * 2] = e[0];
+    entries[(j & 1) * 2 + 1] = e[1];
+    mbar_arrive_expect_tx(f2, L::TILE + (KEYS ? 2 * BM * 4 : 0));
+    for (int p = 0; p < 2; ++p) {
+      const int piece = e[p] & 0x3FFFFFFFu;
+      load(s2, c2, f2, p, piece);
+      if (KEYS) {
+        float* col = reinterpret_cast<float*>(smem + L::OFF_COL) + (j & 1) * 2 * BM + p * 64;
+        bulk_load(col, a.lse2 + t.bh * a.Npad + piece * 64, 256, f2);
+        bulk_load(col + BM, a.delta + t.bh * a.Npad + piece * 64, 256, f2);
+      }
+    }
+    done2 = j + 1;
+  }
+  if (*abort_flag) {
+    // copies still in flight land before the CTA can exit
+    mbar_wait(bars.r_full, 0, a.wait_limit, a.status, nullptr);
+    for (int s = max(done1 - N1, 0); s < done1; ++s)
+      mbar_wait(bars.c1_full + s % N1, (s / N1) & 1, a.wait_limit, a.status, nullptr);
+    for (int s = max(done2 - N2, 0); s < done2; ++s)
+      mbar_wait(bars.c2_full + s % N2, (s / N2) & 1, a.wait_limit, a.status, nullptr);
+  }
+}
+
+// d[128 x 128] = x y^T over d, both operands' rows in shared memory
+template <int D>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t x, uint32_t y) {
+  const uint32_t idesc = idesc_bf16_f32(BM, BM, 0);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
+    umma_ss(d, smem_desc_sw128(x + off, 16, 1024), smem_desc_sw128(y + off, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+  }
+}
+// d[128 x D] += p y, p packed in TMEM (columns 0-63 at p, 64-127 at p + second), y's rows in shared memory
+template <int D>
+__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t p, uint32_t second, uint32_t y, bool first) {
+  const uint32_t idesc = idesc_bf16_f32(BM, D, 1);
+#pragma unroll
+  for (int kk = 0; kk < BM / 16; ++kk)
+    umma_ts(d, p + (kk >> 2) * second + (kk & 3) * 8, smem_desc_sw128(y + kk * 2048, BM * 128, 1024), idesc,
+            (!first || kk > 0) ? 1u : 0u);
+}
+
+// tcgen05.mma instructions of one thread complete in the order of their issue:
+// S of step j + 1 may follow the product that reads P of step j from the same
+// columns, and dP the one that reads dS.
+template <int D, bool KEYS>
+__device__ __forceinline__ void issue(uint8_t* smem, const Bars& bars, uint32_t tmem, const AttendGradArgs& a,
+                                      int n_steps, volatile int* abort_flag) {
+  using L = Layout<D>;
+  const uint32_t r1 = smem_u32(smem + L::OFF_R1), r2 = smem_u32(smem + L::OFF_R2);
+  const uint32_t c1 = smem_u32(smem + L::OFF_C1), c2 = smem_u32(smem + L::OFF_C2);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = mbar_wait(bar, parity, a.wait_limit, a.status, abort_flag);
+    tc_fence_after();
+    return ok;
+  };
+  auto s_of = [&](int j) {
+    if (!wait(bars.c1_full + j % N1, (j / N1) & 1)) return false;
+    mma_rows<D>(tmem + kS, r1, c1 + (j % N1) * L::TILE);
+    umma_commit(bars.s_full);
+    return true;
+  };
+  auto dp_of = [&](int j) {
+    if (!wait(bars.c2_full + (j & 1), (j >> 1) & 1)) return false;
+    mma_rows<D>(tmem + kDP, r2, c2 + (j & 1) * L::TILE);
+    umma_commit(bars.dp_full);
+    return true;
+  };
+  bool ok = n_steps > 0 && wait(bars.r_full, 0) && s_of(0) && dp_of(0);
+  for (int j = 0; ok && j < n_steps; ++j) {
+    const bool more = j + 1 < n_steps;
+    if (!wait(bars.s_done, j & 1)) break;
+    if (KEYS) mma_sum<D>(tmem + kAcc2, tmem + kS, 64, c2 + (j & 1) * L::TILE, j == 0);
+    if (more && !s_of(j + 1)) break;
+    if (KEYS) {
+      if (!wait(bars.ds_full, j & 1)) break;
+      mma_sum<D>(tmem + kAcc1, tmem + kDP, 64, c1 + (j % N1) * L::TILE, j == 0);
+      umma_commit(bars.c_empty + (j & 1));
+      if (more && !dp_of(j + 1)) break;
+    } else {
+      if (!wait(bars.dp_done, j & 1)) break;
+      if (more && !dp_of(j + 1)) break;
+      if (!wait(bars.ds_full, j & 1)) break;
+      mma_sum<D>(tmem + kAcc1, tmem + kDS + (j & 1) * 64, 32, c1 + (j % N1) * L::TILE, j == 0);
+      umma_commit(bars.c_empty + (j & 1));
+    }
+  }
+  // every UMMA has completed before the sums are read and TMEM is released
+  umma_commit(bars.drain);
+  mbar_wait(bars.drain, 0, a.wait_limit, a.status, nullptr);
+}
+
+template <int D, bool KEYS, bool MASKED>
+__device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_t tmem, const AttendGradArgs& a,
+                                        const Tile& t, const uint32_t* entries, float scale_log2, float scale,
+                                        volatile int* abort_flag) {
+  using L = Layout<D>;
+  const int lane = threadIdx.x & 31, wg = threadIdx.x >> 7, row = threadIdx.x & 127;
+  const int half = row >> 6, grow = t.tile * BM + row;
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(row & ~31) << 16);
+  const uint32_t s_col = t_lane + kS + wg * 64, dp_col = t_lane + kDP + wg * 64;
+  const long long wl = a.wait_limit;
+  float lse = 0.f, delta = 0.f;
+  if (!KEYS) {
+    lse = a.lse2[t.bh * a.Npad + grow];
+    delta = a.delta[t.bh * a.Npad + grow];
+  }
+  bool alive = true;
+  for (int j = 0; j < t.n_steps; ++j) {
+    alive = warp_wait(bars.c2_full + (j & 1), (j >> 1) & 1, wl, a.status, abort_flag);
+    if (!alive) break;
+    const uint32_t e = entries[(j & 1) * 2 + wg];
+    const int piece = e & 0x3FFFFFFFu;
+    const bool take = (e >> (30 + half)) & 1u;                       // the same for the warp
+    const int valid = KEYS ? 64 : a.N_valid - piece * 64;            // columns that exist (may exceed 64)
+    uint64_t set = ~0ull;                                            // per-token lists
+    if (MASKED && take)
+      set = KEYS ? __ldg(a.masks_t + (t.bh * a.nB + t.tile * 2 + half) * a.nB + piece)
+                 : __ldg(a.masks_t + (t.bh * a.nB + piece) * a.nB + t.tile * 2 + half);
+    const float* col = reinterpret_cast<const float*>(smem + L::OFF_COL) + (j & 1) * 2 * BM + wg * 64;
+    alive = warp_wait(bars.s_full, j & 1, wl, a.status, abort_flag);
+    if (!alive) break;
+    tc_fence_after();
+    uint32_t r[64];
+    tmem_ld32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+    tmem_ld32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+    tmem_wait_ld_dep(*reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+    reg_dep(*reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+    if (!KEYS) warp_arrive(bars.s_done, lane);                       // the S columns are free
+    // r: P in fp32
+    const unsigned long long sc2 = f2_as_u64(scale_log2, scale_log2);
+    if (take) {
+      if (KEYS) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(col + c);
+          float p[4];
+          u64_as_f2(ffma2(f2_as_u64(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, f2_as_u64(-l4.x, -l4.y)), p[0], p[1]);
+          u64_as_f2(ffma2(f2_as_u64(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sc2, f2_as_u64(-l4.z, -l4.w)), p[2], p[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x = ex2(p[i]);
+            if (MASKED) x = ((set >> (c + i)) & 1ull) ? x : 0.f;
+            r[c + i] = __float_as_uint(x);
+          }
+        }
+      } else {
+        const unsigned long long nl2 = f2_as_u64(-lse, -lse);
+        const bool mine = !MASKED || ((set >> (row & 63)) & 1ull);
+        const int n = MASKED && !mine ? 0 : valid;
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float p0, p1;
+          u64_as_f2(ffma2(f2_as_u64(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, nl2), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          r[c] = __float_as_uint(c < n ? p0 : 0.f);
+          r[c + 1] = __float_as_uint(c + 1 < n ? p1 : 0.f);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 64; ++c) r[c] = 0u;
+    }
+    if (KEYS) {
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
+      tmem_st32(s_col, pk);
+      tmem_wait_st();
+      warp_arrive(bars.s_done, lane);
+    }
+    alive = warp_wait(bars.dp_full, j & 1, wl, a.status, abort_flag);
+    if (!alive) break;
+    tc_fence_after();
+    uint32_t pk[32];
+    uint32_t g[64];
+    tmem_ld32(dp_col, *reinterpret_cast<uint32_t(*)[32]>(&g[0]));
+    tmem_ld32(dp_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&g[32]));
+    tmem_wait_ld_dep(*reinterpret_cast<uint32_t(*)[32]>(&g[0]));
+    reg_dep(*reinterpret_cast<uint32_t(*)[32]>(&g[32]));
+    if (!KEYS) warp_arrive(bars.dp_done, lane);                      // the dP columns are free
+    // a pair without probability gets 0, whatever its dP holds
+#pragma unroll
+    for (int c = 0; c < 64; c += 4) {
+      float4 d4 = make_float4(delta, delta, delta, delta);
+      if (KEYS) d4 = *reinterpret_cast<const float4*>(col + BM + c);
+      const float dd[4] = {d4.x, d4.y, d4.z, d4.w};
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float p = __uint_as_float(r[c + i]);
+        x[i] = p * (__uint_as_float(g[c + i]) - dd[i]);
+        if (MASKED || !take || (!KEYS && valid < 64)) x[i] = p == 0.f ? 0.f : x[i];
+      }
+      pk[c / 2] = pack_bf16x2(x[0], x[1]);
+      pk[c / 2 + 1] = pack_bf16x2(x[2], x[3]);
+    }
+    tmem_st32(KEYS ? dp_col : t_lane + kDS + (j & 1) * 64 + wg * 32, pk);
+    tmem_wait_st();
+    warp_arrive(bars.ds_full, lane);
+  }
+  // ---- the rows' sums
+  bool sums = alive && t.n_steps > 0;
+  if (sums) {
+    sums = warp_wait(bars.drain, 0, wl, a.status, abort_flag);
+    tc_fence_after();
+  }
+  const bool valid = grow < a.N_valid;
+  auto store = [&](uint32_t acc, void* out, const GradStride& st, float f) {
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out) + t.b * st.b + t.h * st.h + grow * st.n + wg * (D / 2);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      uint32_t o[32];
+      if (sums) {
+        tmem_ld32(t_lane + acc + wg * (D / 2) + c * 32, o);
+        tmem_wait_ld_dep(o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0u;
+      }
+      if (valid) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<uint4*>(dst + c * 32)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+      }
+    }
+  };
+  if (KEYS) {
+    store(kAcc1, a.dk, a.st[kDk], scale);
+    store(kAcc2, a.dv, a.st[kDv], 1.f);
+  } else {
+    store(kAcc1, a.dq, a.st[kDq], scale);
+  }
+}
+
+template <int D, bool KEYS, bool MASKED>
+__device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, const CUtensorMap* tk,
+                                         const CUtensorMap* tv, const CUtensorMap* tdo, const AttendGradArgs& a, int tile,
+                                         float scale_log2, float scale) {
+  using L = Layout<D>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Bars bars = make_bars(smem + L::OFF_BAR);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  uint32_t* entries = misc + 4;
+  if (threadIdx.x == 0) {
+    uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+    for (int i = 0; i < 14; ++i) mbar_init(b + i, (i >= 10 && i <= 12) ? 8 : 1);   // s_done, dp_done, ds_full: eight warps
+    misc[1] = 0;
+    misc[2] = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(misc, kTmemCols);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  // the tile's kept pieces: the set bits of its blocks' rows, one row for 128-token blocks
+  const int shift = a.block == 128 ? 1 : 0, W = (a.nB + 31) >> 5;
+  Tile t;
+  t.tile = tile;
+  t.h = blockIdx.y;
+  t.b = blockIdx.z;
+  t.bh = static_cast<long long>(t.b) * a.H + t.h;
+  const uint32_t* rows = KEYS ? a.bits_t : a.bits;
+  const int first = shift ? tile : 2 * tile;
+  const uint32_t* row0 = rows + (t.bh * a.nB + first) * W;
+  const uint32_t* row1 = !shift && first + 1 < a.nB ? row0 + W : nullptr;
+  if (threadIdx.x < 128) {
+    int n = 0;
+    for (int w = threadIdx.x; w < W; w += 128) n += __popc(__ldg(row0 + w) | (row1 ? __ldg(row1 + w) : 0u));
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0 && n) atomicAdd(misc + 2, static_cast<uint32_t>(n));
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  t.n_steps = ((static_cast<int>(misc[2]) << shift) + 1) >> 1;
+  if (warp == 8) {
+    if (lane == 0) {
+      Walk walk;
+      walk.init(row0, row1, W, shift);
+      if (KEYS) produce<D, KEYS>(smem, bars, tk, tv, tq, tdo, a, t, walk, entries, abort_flag);
+      else produce<D, KEYS>(smem, bars, tq, tdo, tk, tv, a, t, walk, entries, abort_flag);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) issue<D, KEYS>(smem, bars, tmem, a, t.n_steps, abort_flag);
+  } else {
+    softmax<D, KEYS, MASKED>(smem, bars, tmem, a, t, entries, scale_log2, scale, abort_flag);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool MASKED>
+__global__ void __launch_bounds__(kThreads, 1)
+attend_grad_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                      const __grid_constant__ AttendGradArgs a, int tiles, float scale_log2, float scale) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // a CTA of this launch already gave up on a wait: skip the work, the call has failed
+  if (*reinterpret_cast<volatile int32_t*>(a.status) == LBSA_ERR_TIMEOUT) return;
+  if (static_cast<int>(blockIdx.x) < tiles) run_tile<D, true, MASKED>(smem, &tq, &tk, &tv, &tdo, a, blockIdx.x, scale_log2, scale);
+  else run_tile<D, false, MASKED>(smem, &tq, &tk, &tv, &tdo, a, blockIdx.x - tiles, scale_log2, scale);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_grad_tc(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
+                                  const CUtensorMap* tdo, const AttendGradArgs& a, cudaStream_t s) {
+  const int tiles = (a.N_valid + BM - 1) / BM;
+  const double scale = 1.0 / std::sqrt(static_cast<double>(a.d));
+  auto go = [&](auto kern, int smem) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3(2 * tiles, a.H, a.B), kThreads, smem, s>>>(*tq, *tk, *tv, *tdo, a, tiles,
+                                                          static_cast<float>(1.4426950408889634 * scale),
+                                                          static_cast<float>(scale));
+    return cudaGetLastError();
+  };
+  if (a.d == 128)
+    return a.masks ? go(attend_grad_tc_kernel<128, true>, Layout<128>::BYTES)
+                   : go(attend_grad_tc_kernel<128, false>, Layout<128>::BYTES);
+  return a.masks ? go(attend_grad_tc_kernel<64, true>, Layout<64>::BYTES)
+                 : go(attend_grad_tc_kernel<64, false>, Layout<64>::BYTES);
+}
+
+}  // namespace lbsa

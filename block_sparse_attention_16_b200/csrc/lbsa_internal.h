@@ -171,8 +171,11 @@ struct AttendGradArgs {
 size_t attend_grad_workspace(AttendGradArgs* a, void* base);
 cudaError_t launch_attend_grad_prep(const void* out, const void* dout, const float* lse, int dtype,
                                     const AttendGradArgs& a, cudaStream_t s);
-cudaError_t launch_attend_grad_simt(const void* q, const void* k, const void* v, const void* dout, int dtype,
-                                    const AttendGradArgs& a, cudaStream_t s);
+// bf16 on the tensor cores (attend_grad_tc.cu); the maps' boxes are 64 columns x 64 rows
+cudaError_t launch_attend_grad_tc(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
+                                  const CUtensorMap* tdo, const AttendGradArgs& a, cudaStream_t s);
+cudaError_t launch_attend_grad_f32(const float* q, const float* k, const float* v, const float* dout,
+                                   const AttendGradArgs& a, cudaStream_t s);
 
 // rotary positions and the per-head norm (rope.cu); strides are in elements: batch, head, row
 struct RopeItem {
