@@ -13,9 +13,9 @@
 // fp32 gradient buffer in memory and no order between CTAs: the same inputs
 // give the same bits.
 //
-// Tables (scratch of the call): lse in log2 units and D, padded to whole
-// 128-row tiles (a row that keeps nothing, or does not exist, gets lse = +inf
-// and D = 0, so that its P is 0 without a test), and the kept pairs as bits in
+// Tables (scratch of the call): -lse in log2 units and -D, padded to whole
+// 128-row tiles (a row that keeps nothing, or does not exist, gets -inf and 0,
+// so that its P is 0 without a test), and the kept pairs as bits in
 // both directions; the per-token sets go to [key block][query block].
 #include "lbsa_device.cuh"
 
@@ -103,8 +103,8 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
   }
   if (lane == 0) {
     const bool none = l == -INFINITY;
-    a.lse2[row] = none ? INFINITY : l * kLog2e;
-    a.delta[row] = none ? 0.f : sum;
+    a.neg_lse2[row] = none ? -INFINITY : -l * kLog2e;
+    a.neg_delta[row] = none ? 0.f : -sum;
   }
 }
 
@@ -238,9 +238,9 @@ __global__ void __launch_bounds__(256) attend_grad_f32_kernel(const float* __res
             const int qi = keys ? col : row, ki = keys ? row : col;              // within their pieces
             const int qn = (keys ? c0 : r0) + qi, kn = (keys ? r0 : c0) + ki;
             const bool on = kn < N && ((set >> qi) & 1ull);
-            const float pr = on ? exp2f(fmaf(p[i][j], scale2, -a.lse2[bh * a.Npad + qn])) : 0.f;
+            const float pr = on ? exp2f(fmaf(p[i][j], scale2, a.neg_lse2[bh * a.Npad + qn])) : 0.f;
             sp[row * kPitch + col] = pr;
-            sd[row * kPitch + col] = on ? pr * (g[i][j] - a.delta[bh * a.Npad + qn]) : 0.f;
+            sd[row * kPitch + col] = on ? pr * (g[i][j] + a.neg_delta[bh * a.Npad + qn]) : 0.f;
           }
         __syncthreads();
         weighted<D>(acc1, sd, c1, ty, tx);
@@ -296,8 +296,8 @@ size_t attend_grad_workspace(AttendGradArgs* a, void* base) {
   p[3] = take(bh * a->nB * W * sizeof(uint32_t));
   p[4] = a->masks ? take(bh * a->nB * a->nB * sizeof(uint64_t)) : nullptr;
   if (base) {
-    a->lse2 = reinterpret_cast<float*>(p[0]);
-    a->delta = reinterpret_cast<float*>(p[1]);
+    a->neg_lse2 = reinterpret_cast<float*>(p[0]);
+    a->neg_delta = reinterpret_cast<float*>(p[1]);
     a->bits = reinterpret_cast<uint32_t*>(p[2]);
     a->bits_t = reinterpret_cast<uint32_t*>(p[3]);
     a->masks_t = reinterpret_cast<uint64_t*>(p[4]);

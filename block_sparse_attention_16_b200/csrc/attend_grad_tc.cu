@@ -29,7 +29,17 @@ namespace lbsa {
 namespace {
 
 constexpr int BM = 128;             // rows of a tile, columns of a step
-constexpr int kThreads = 320;
+#ifndef LBSA_GRAD_GROUPS
+#define LBSA_GRAD_GROUPS 4
+#endif
+#ifndef LBSA_GRAD_POLY8
+#define LBSA_GRAD_POLY8 0
+#endif
+constexpr int kGroups = LBSA_GRAD_GROUPS;        // softmax warpgroups, kCols columns of a step each
+constexpr int kCols = BM / kGroups;
+constexpr int kPoly8 = LBSA_GRAD_POLY8;
+constexpr int kProducer = kGroups * 4, kIssuer = kProducer + 1;     // their warps
+constexpr int kThreads = (kIssuer + 1) * 32;
 constexpr int N1 = 3, N2 = 2;       // ring depths of the two operands
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kS = 0, kDP = 128, kAcc1 = 256, kAcc2 = 384, kDS = 384;
@@ -46,8 +56,9 @@ struct Layout {
 };
 
 struct Bars {
-  uint64_t *r_full, *c1_full, *c2_full, *c_empty, *s_full, *dp_full, *s_done, *dp_done, *ds_full, *drain;
+  uint64_t *r_full, *c1_full, *c2_full, *c_empty, *s_full, *dp_full, *drain, *s_done, *dp_done, *ds_full;
 };
+constexpr int kBars = 15, kWarpBars = 11;      // from kWarpBars on every softmax warp arrives
 __device__ __forceinline__ Bars make_bars(uint8_t* base) {
   uint64_t* b = reinterpret_cast<uint64_t*>(base);
   return Bars{b, b + 1, b + 4, b + 6, b + 8, b + 9, b + 10, b + 11, b + 12, b + 13};
@@ -149,8 +160,8 @@ __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const C
       load(s2, c2, f2, p, piece);
       if (KEYS) {
         float* col = reinterpret_cast<float*>(smem + L::OFF_COL) + (j & 1) * 2 * BM + p * 64;
-        bulk_load(col, a.lse2 + t.bh * a.Npad + piece * 64, 256, f2);
-        bulk_load(col + BM, a.delta + t.bh * a.Npad + piece * 64, 256, f2);
+        bulk_load(col, a.neg_lse2 + t.bh * a.Npad + piece * 64, 256, f2);
+        bulk_load(col + BM, a.neg_delta + t.bh * a.Npad + piece * 64, 256, f2);
       }
     }
     done2 = j + 1;
@@ -165,26 +176,33 @@ __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const C
   }
 }
 
-// d[128 x 128] = x y^T over d, both operands' rows in shared memory
+// d[128 x 128] = x y^T over d; x, y: descriptors of K-major rows in shared memory
 template <int D>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t x, uint32_t y) {
-  const uint32_t idesc = idesc_bf16_f32(BM, BM, 0);
+__device__ __forceinline__ void mma_rows(uint32_t d, uint64_t x, uint64_t y) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
-    umma_ss(d, smem_desc_sw128(x + off, 16, 1024), smem_desc_sw128(y + off, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+    const uint64_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
+    umma_ss(d, x + off, y + off, idesc_bf16_f32(BM, BM, 0), kk > 0 ? 1u : 0u);
   }
 }
-// d[128 x D] += p y, p packed in TMEM (columns 0-63 at p, 64-127 at p + second), y's rows in shared memory
+// d[128 x D] += p y; p packed in TMEM (each warpgroup's kCols columns start `pitch` further), y: MN-major rows
 template <int D>
-__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t p, uint32_t second, uint32_t y, bool first) {
-  const uint32_t idesc = idesc_bf16_f32(BM, D, 1);
+__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t p, uint32_t pitch, uint64_t y, bool first) {
+  constexpr int PER = kCols / 16;
 #pragma unroll
   for (int kk = 0; kk < BM / 16; ++kk)
-    umma_ts(d, p + (kk >> 2) * second + (kk & 3) * 8, smem_desc_sw128(y + kk * 2048, BM * 128, 1024), idesc,
+    umma_ts(d, p + (kk / PER) * pitch + (kk % PER) * 8, y + kk * (2048 >> 4), idesc_bf16_f32(BM, D, 1),
             (!first || kk > 0) ? 1u : 0u);
 }
 
+// The whole warp walks the steps, so that addresses and descriptors stay
+// warp-uniform, and one elected lane issues: with a single lane in the loop the
+// operands went through per-thread registers and an instruction took about 100
+// cycles to issue, where the tensor core needs 64 for it.
+// ds_full is a pair: dP of step j + 1 is issued before dS of step j is waited
+// for (queries), so the softmax warps may finish step j + 1's dS first, and on
+// one barrier the phase of step j would then be missed.  Every other barrier's
+// next phase needs an instruction that follows the wait for the last one.
 // tcgen05.mma instructions of one thread complete in the order of their issue:
 // S of step j + 1 may follow the product that reads P of step j from the same
 // columns, and dP the one that reads dS.
@@ -192,47 +210,118 @@ template <int D, bool KEYS>
 __device__ __forceinline__ void issue(uint8_t* smem, const Bars& bars, uint32_t tmem, const AttendGradArgs& a,
                                       int n_steps, volatile int* abort_flag) {
   using L = Layout<D>;
-  const uint32_t r1 = smem_u32(smem + L::OFF_R1), r2 = smem_u32(smem + L::OFF_R2);
-  const uint32_t c1 = smem_u32(smem + L::OFF_C1), c2 = smem_u32(smem + L::OFF_C2);
+  const uint64_t r1 = smem_desc_sw128(smem_u32(smem + L::OFF_R1), 16, 1024), r2 = r1 + ((L::OFF_R2 - L::OFF_R1) >> 4);
+  const uint64_t c1 = r1 + ((L::OFF_C1 - L::OFF_R1) >> 4), c2 = r1 + ((L::OFF_C2 - L::OFF_R1) >> 4);
+  const uint64_t m1 = smem_desc_sw128(smem_u32(smem + L::OFF_C1), BM * 128, 1024), m2 = m1 + ((L::OFF_C2 - L::OFF_C1) >> 4);
+  constexpr uint64_t STAGE = L::TILE >> 4;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = mbar_wait(bar, parity, a.wait_limit, a.status, abort_flag);
+    const bool ok = warp_wait(bar, parity, a.wait_limit, a.status, abort_flag);
     tc_fence_after();
     return ok;
   };
-  auto s_of = [&](int j) {
-    if (!wait(bars.c1_full + j % N1, (j / N1) & 1)) return false;
-    mma_rows<D>(tmem + kS, r1, c1 + (j % N1) * L::TILE);
-    umma_commit(bars.s_full);
+  int st = 0, st_next = 0, ph_next = 0;         // first operand's ring: this step's stage; the next S's stage and phase
+  auto s_of = [&](int) {
+    if (!wait(bars.c1_full + st_next, ph_next)) return false;
+    if (elect_one()) {
+      mma_rows<D>(tmem + kS, r1, c1 + st_next * STAGE);
+      umma_commit(bars.s_full);
+    }
+    __syncwarp();
+    st = st_next;
+    if (++st_next == N1) {
+      st_next = 0;
+      ph_next ^= 1;
+    }
     return true;
   };
   auto dp_of = [&](int j) {
     if (!wait(bars.c2_full + (j & 1), (j >> 1) & 1)) return false;
-    mma_rows<D>(tmem + kDP, r2, c2 + (j & 1) * L::TILE);
-    umma_commit(bars.dp_full);
+    if (elect_one()) {
+      mma_rows<D>(tmem + kDP, r2, c2 + (j & 1) * STAGE);
+      umma_commit(bars.dp_full);
+    }
+    __syncwarp();
     return true;
   };
   bool ok = n_steps > 0 && wait(bars.r_full, 0) && s_of(0) && dp_of(0);
   for (int j = 0; ok && j < n_steps; ++j) {
     const bool more = j + 1 < n_steps;
+    const int mine = st;                        // step j's stage of the first operand
     if (!wait(bars.s_done, j & 1)) break;
-    if (KEYS) mma_sum<D>(tmem + kAcc2, tmem + kS, 64, c2 + (j & 1) * L::TILE, j == 0);
-    if (more && !s_of(j + 1)) break;
     if (KEYS) {
-      if (!wait(bars.ds_full, j & 1)) break;
-      mma_sum<D>(tmem + kAcc1, tmem + kDP, 64, c1 + (j % N1) * L::TILE, j == 0);
-      umma_commit(bars.c_empty + (j & 1));
-      if (more && !dp_of(j + 1)) break;
-    } else {
+      if (elect_one()) mma_sum<D>(tmem + kAcc2, tmem + kS, kCols, m2 + (j & 1) * STAGE, j == 0);
+      __syncwarp();
+    }
+    if (more && !s_of(j + 1)) break;
+    if (!KEYS) {
       if (!wait(bars.dp_done, j & 1)) break;
       if (more && !dp_of(j + 1)) break;
-      if (!wait(bars.ds_full, j & 1)) break;
-      mma_sum<D>(tmem + kAcc1, tmem + kDS + (j & 1) * 64, 32, c1 + (j % N1) * L::TILE, j == 0);
+    }
+    if (!wait(bars.ds_full + (j & 1), (j >> 1) & 1)) break;
+    if (elect_one()) {
+      if (KEYS) mma_sum<D>(tmem + kAcc1, tmem + kDP, kCols, m1 + mine * STAGE, j == 0);
+      else mma_sum<D>(tmem + kAcc1, tmem + kDS + (j & 1) * 64, kCols / 2, m1 + mine * STAGE, j == 0);
       umma_commit(bars.c_empty + (j & 1));
     }
+    __syncwarp();
+    if (KEYS && more && !dp_of(j + 1)) break;
   }
   // every UMMA has completed before the sums are read and TMEM is released
-  umma_commit(bars.drain);
+  if (elect_one()) umma_commit(bars.drain);
+  __syncwarp();
   mbar_wait(bars.drain, 0, a.wait_limit, a.status, nullptr);
+}
+
+// P of CPT columns in place of their logits (r), then dS = P (dP - D) in place
+// of dP.  neg_lse / neg_delta: of the columns (keys) or of the row (queries).
+template <int CPT, bool KEYS>
+__device__ __forceinline__ void probabilities(uint32_t (&r)[CPT], const float* neg_lse, float row_neg_lse, float scale_log2) {
+  const unsigned long long sc2 = f2_as_u64(scale_log2, scale_log2);
+#pragma unroll
+  for (int c = 0; c < CPT; c += 4) {
+    ulonglong2 l = make_ulonglong2(f2_as_u64(row_neg_lse, row_neg_lse), f2_as_u64(row_neg_lse, row_neg_lse));
+    if (KEYS) l = *reinterpret_cast<const ulonglong2*>(neg_lse + c);
+    float v[4];
+    u64_as_f2(ffma2(f2_as_u64(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, l.x), v[0], v[1]);
+    u64_as_f2(ffma2(f2_as_u64(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sc2, l.y), v[2], v[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[c + i] = __float_as_uint((c / 4 * kPoly8) % 8 < kPoly8 && i < 2 ? exp2_poly3(v[i]) : ex2(v[i]));
+  }
+}
+template <int CPT, bool KEYS>
+__device__ __forceinline__ void score_gradients(uint32_t (&g)[CPT], const uint32_t (&p)[CPT], const float* neg_delta,
+                                                float row_neg_delta) {
+#pragma unroll
+  for (int c = 0; c < CPT; c += 4) {
+    ulonglong2 d = make_ulonglong2(f2_as_u64(row_neg_delta, row_neg_delta), f2_as_u64(row_neg_delta, row_neg_delta));
+    if (KEYS) d = *reinterpret_cast<const ulonglong2*>(neg_delta + c);
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const unsigned long long x =
+          fmul2(fadd2(f2_as_u64(__uint_as_float(g[c + i]), __uint_as_float(g[c + i + 1])), i ? d.y : d.x),
+                f2_as_u64(__uint_as_float(p[c + i]), __uint_as_float(p[c + i + 1])));
+      g[c + i] = static_cast<uint32_t>(x);
+      g[c + i + 1] = static_cast<uint32_t>(x >> 32);
+    }
+  }
+}
+
+template <int CPT>
+__device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&r)[CPT]) {
+#pragma unroll
+  for (int c = 0; c < CPT; c += 32) tmem_ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&r[c]));
+  tmem_wait_ld_dep(*reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+  if (CPT == 64) reg_dep(*reinterpret_cast<uint32_t(*)[32]>(&r[CPT - 32]));
+}
+// rounded to bf16, two a column
+template <int CPT>
+__device__ __forceinline__ void store_packed(uint32_t taddr, const uint32_t (&r)[CPT]) {
+  uint32_t pk[CPT / 2];
+#pragma unroll
+  for (int c = 0; c < CPT / 2; ++c) pk[c] = pack_bf16x2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
+  if constexpr (CPT == 64) tmem_st32(taddr, pk);
+  else tmem_st16(taddr, pk);
+  tmem_wait_st();
 }
 
 template <int D, bool KEYS, bool MASKED>
@@ -240,110 +329,66 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
                                         const Tile& t, const uint32_t* entries, float scale_log2, float scale,
                                         volatile int* abort_flag) {
   using L = Layout<D>;
+  constexpr int CPT = kCols;
   const int lane = threadIdx.x & 31, wg = threadIdx.x >> 7, row = threadIdx.x & 127;
   const int half = row >> 6, grow = t.tile * BM + row;
+  const int c0 = wg * CPT, p = c0 >> 6, in_piece = c0 & 63;          // the thread's columns, their piece of the step
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(row & ~31) << 16);
-  const uint32_t s_col = t_lane + kS + wg * 64, dp_col = t_lane + kDP + wg * 64;
+  const uint32_t s_col = t_lane + kS + c0, dp_col = t_lane + kDP + c0;
   const long long wl = a.wait_limit;
-  float lse = 0.f, delta = 0.f;
+  float neg_lse = 0.f, neg_delta = 0.f;
   if (!KEYS) {
-    lse = a.lse2[t.bh * a.Npad + grow];
-    delta = a.delta[t.bh * a.Npad + grow];
+    neg_lse = a.neg_lse2[t.bh * a.Npad + grow];
+    neg_delta = a.neg_delta[t.bh * a.Npad + grow];
   }
   bool alive = true;
   for (int j = 0; j < t.n_steps; ++j) {
     alive = warp_wait(bars.c2_full + (j & 1), (j >> 1) & 1, wl, a.status, abort_flag);
     if (!alive) break;
-    const uint32_t e = entries[(j & 1) * 2 + wg];
+    const uint32_t e = entries[(j & 1) * 2 + p];
     const int piece = e & 0x3FFFFFFFu;
     const bool take = (e >> (30 + half)) & 1u;                       // the same for the warp
-    const int valid = KEYS ? 64 : a.N_valid - piece * 64;            // columns that exist (may exceed 64)
-    uint64_t set = ~0ull;                                            // per-token lists
-    if (MASKED && take)
-      set = KEYS ? __ldg(a.masks_t + (t.bh * a.nB + t.tile * 2 + half) * a.nB + piece)
-                 : __ldg(a.masks_t + (t.bh * a.nB + piece) * a.nB + t.tile * 2 + half);
-    const float* col = reinterpret_cast<const float*>(smem + L::OFF_COL) + (j & 1) * 2 * BM + wg * 64;
+    // the thread's columns that count, as bits from bit 0
+    uint64_t on = ~0ull;
+    if (MASKED && take) {
+      if (KEYS) on = __ldg(a.masks_t + (t.bh * a.nB + t.tile * 2 + half) * a.nB + piece) >> in_piece;
+      else on = ((__ldg(a.masks_t + (t.bh * a.nB + piece) * a.nB + t.tile * 2 + half) >> (row & 63)) & 1ull) ? ~0ull : 0ull;
+    }
+    if (!KEYS) {
+      const int valid = a.N_valid - piece * 64 - in_piece;
+      if (valid < CPT) on &= valid > 0 ? (1ull << valid) - 1ull : 0ull;
+    }
+    if (!take) on = 0ull;
+    const bool all = !MASKED && take && (KEYS || a.N_valid - piece * 64 - in_piece >= CPT);   // the same for the warp
+    const float* col = reinterpret_cast<const float*>(smem + L::OFF_COL) + (j & 1) * 2 * BM + c0;
     alive = warp_wait(bars.s_full, j & 1, wl, a.status, abort_flag);
     if (!alive) break;
     tc_fence_after();
-    uint32_t r[64];
-    tmem_ld32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-    tmem_ld32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-    tmem_wait_ld_dep(*reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-    reg_dep(*reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+    uint32_t r[CPT], g[CPT];
+    load_cols<CPT>(s_col, r);
     if (!KEYS) warp_arrive(bars.s_done, lane);                       // the S columns are free
-    // r: P in fp32
-    const unsigned long long sc2 = f2_as_u64(scale_log2, scale_log2);
-    if (take) {
-      if (KEYS) {
+    probabilities<CPT, KEYS>(r, col, neg_lse, scale_log2);
+    if (!all) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 l4 = *reinterpret_cast<const float4*>(col + c);
-          float p[4];
-          u64_as_f2(ffma2(f2_as_u64(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, f2_as_u64(-l4.x, -l4.y)), p[0], p[1]);
-          u64_as_f2(ffma2(f2_as_u64(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sc2, f2_as_u64(-l4.z, -l4.w)), p[2], p[3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x = ex2(p[i]);
-            if (MASKED) x = ((set >> (c + i)) & 1ull) ? x : 0.f;
-            r[c + i] = __float_as_uint(x);
-          }
-        }
-      } else {
-        const unsigned long long nl2 = f2_as_u64(-lse, -lse);
-        const bool mine = !MASKED || ((set >> (row & 63)) & 1ull);
-        const int n = MASKED && !mine ? 0 : valid;
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float p0, p1;
-          u64_as_f2(ffma2(f2_as_u64(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sc2, nl2), p0, p1);
-          p0 = ex2(p0);
-          p1 = ex2(p1);
-          r[c] = __float_as_uint(c < n ? p0 : 0.f);
-          r[c + 1] = __float_as_uint(c + 1 < n ? p1 : 0.f);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 64; ++c) r[c] = 0u;
+      for (int c = 0; c < CPT; ++c) r[c] = ((on >> c) & 1ull) ? r[c] : 0u;
     }
     if (KEYS) {
-      uint32_t pk[32];
-#pragma unroll
-      for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
-      tmem_st32(s_col, pk);
-      tmem_wait_st();
+      store_packed<CPT>(s_col, r);
       warp_arrive(bars.s_done, lane);
     }
     alive = warp_wait(bars.dp_full, j & 1, wl, a.status, abort_flag);
     if (!alive) break;
     tc_fence_after();
-    uint32_t pk[32];
-    uint32_t g[64];
-    tmem_ld32(dp_col, *reinterpret_cast<uint32_t(*)[32]>(&g[0]));
-    tmem_ld32(dp_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&g[32]));
-    tmem_wait_ld_dep(*reinterpret_cast<uint32_t(*)[32]>(&g[0]));
-    reg_dep(*reinterpret_cast<uint32_t(*)[32]>(&g[32]));
+    load_cols<CPT>(dp_col, g);
     if (!KEYS) warp_arrive(bars.dp_done, lane);                      // the dP columns are free
-    // a pair without probability gets 0, whatever its dP holds
+    score_gradients<CPT, KEYS>(g, r, col + BM, neg_delta);
+    if (!all) {
+      // a pair that is not kept gets 0, whatever its dP holds
 #pragma unroll
-    for (int c = 0; c < 64; c += 4) {
-      float4 d4 = make_float4(delta, delta, delta, delta);
-      if (KEYS) d4 = *reinterpret_cast<const float4*>(col + BM + c);
-      const float dd[4] = {d4.x, d4.y, d4.z, d4.w};
-      float x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = __uint_as_float(r[c + i]);
-        x[i] = p * (__uint_as_float(g[c + i]) - dd[i]);
-        if (MASKED || !take || (!KEYS && valid < 64)) x[i] = p == 0.f ? 0.f : x[i];
-      }
-      pk[c / 2] = pack_bf16x2(x[0], x[1]);
-      pk[c / 2 + 1] = pack_bf16x2(x[2], x[3]);
+      for (int c = 0; c < CPT; ++c) g[c] = ((on >> c) & 1ull) ? g[c] : 0u;
     }
-    tmem_st32(KEYS ? dp_col : t_lane + kDS + (j & 1) * 64 + wg * 32, pk);
-    tmem_wait_st();
-    warp_arrive(bars.ds_full, lane);
+    store_packed<CPT>(KEYS ? dp_col : t_lane + kDS + (j & 1) * 64 + wg * (CPT / 2), g);
+    warp_arrive(bars.ds_full + (j & 1), lane);
   }
   // ---- the rows' sums
   bool sums = alive && t.n_steps > 0;
@@ -353,12 +398,11 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
   }
   const bool valid = grow < a.N_valid;
   auto store = [&](uint32_t acc, void* out, const GradStride& st, float f) {
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out) + t.b * st.b + t.h * st.h + grow * st.n + wg * (D / 2);
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out) + t.b * st.b + t.h * st.h + grow * st.n;
+    for (int c = wg * 32; c < D; c += kGroups * 32) {
       uint32_t o[32];
       if (sums) {
-        tmem_ld32(t_lane + acc + wg * (D / 2) + c * 32, o);
+        tmem_ld32(t_lane + acc + c, o);
         tmem_wait_ld_dep(o);
       } else {
 #pragma unroll
@@ -370,7 +414,7 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
         for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          reinterpret_cast<uint4*>(dst + c * 32)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+          reinterpret_cast<uint4*>(dst + c)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
       }
     }
   };
@@ -394,12 +438,12 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
   uint32_t* entries = misc + 4;
   if (threadIdx.x == 0) {
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-    for (int i = 0; i < 14; ++i) mbar_init(b + i, (i >= 10 && i <= 12) ? 8 : 1);   // s_done, dp_done, ds_full: eight warps
+    for (int i = 0; i < kBars; ++i) mbar_init(b + i, i >= kWarpBars ? kGroups * 4 : 1);
     misc[1] = 0;
     misc[2] = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == kIssuer) {
     tmem_alloc(misc, kTmemCols);
     tmem_relinquish();
   }
@@ -426,21 +470,21 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
   tc_fence_after();
   const uint32_t tmem = misc[0];
   t.n_steps = ((static_cast<int>(misc[2]) << shift) + 1) >> 1;
-  if (warp == 8) {
+  if (warp == kProducer) {
     if (lane == 0) {
       Walk walk;
       walk.init(row0, row1, W, shift);
       if (KEYS) produce<D, KEYS>(smem, bars, tk, tv, tq, tdo, a, t, walk, entries, abort_flag);
       else produce<D, KEYS>(smem, bars, tq, tdo, tk, tv, a, t, walk, entries, abort_flag);
     }
-  } else if (warp == 9) {
-    if (lane == 0) issue<D, KEYS>(smem, bars, tmem, a, t.n_steps, abort_flag);
+  } else if (warp == kIssuer) {
+    issue<D, KEYS>(smem, bars, tmem, a, t.n_steps, abort_flag);
   } else {
     softmax<D, KEYS, MASKED>(smem, bars, tmem, a, t, entries, scale_log2, scale, abort_flag);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kIssuer) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }

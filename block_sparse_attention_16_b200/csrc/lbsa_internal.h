@@ -161,8 +161,8 @@ struct AttendGradArgs {
   long long wait_limit;
   // the call's tables (attend_grad_workspace)
   int Npad;                     // N_valid rounded up to whole 128-row tiles
-  float* lse2;                  // [B*H][Npad] lse in log2 units; +inf: the row keeps nothing
-  float* delta;                 // [B*H][Npad] sum of dout * out
+  float* neg_lse2;              // [B*H][Npad] -lse in log2 units; -inf: the row keeps nothing
+  float* neg_delta;             // [B*H][Npad] -sum of dout * out
   uint32_t* bits;               // [B*H][nB queries][ceil(nB / 32)] kept key blocks
   uint32_t* bits_t;             // [B*H][nB keys][ceil(nB / 32)] query blocks that keep it
   uint64_t* masks_t;            // [B*H][nB keys][nB queries], written where bits are set
