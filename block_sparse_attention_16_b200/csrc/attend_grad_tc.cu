@@ -15,14 +15,18 @@
 //   warps 0-3, 4-7  thread t owns row t % 128 = TMEM lane; the first four warps
 //             take a step's first piece (columns 0-63), the others the second.
 //             P = 2^(S scale - lse), packed to bf16 over the S columns just
-//             read (keys); dS = P (dP - D), over the dP columns (keys) or into
-//             one of two buffers (queries), and at the end the rows' sums.
+//             read (keys); dS = P (dP - D), over the dP columns; at the end the
+//             rows' sums.
 //   warp 8    TMA producer: walks the two bit rows, loads the CTA's own tiles
 //             once, then the first operand's pieces through a 3-stage and the
-//             second's (with lse and D of the columns) through a 2-stage ring.
+//             second's through a 2-stage ring, each refilled when its own last
+//             product is done (keys: with lse and D of the columns).
 //   warp 9    UMMA issuer.
-// TMEM columns: [0,128) S, [128,256) dP, [256,256+D) dK or dQ, [384,384+D) dV,
-// or two dS buffers of 64 (queries).
+// TMEM columns: [0,128) S, [128,256) dP, [256,256+D) dK or dQ, [384,384+D) dV.
+// A query tile has no dV: its q and dout rows take those columns, so that all
+// three of its products read their A operand from TMEM.  With both operands in
+// shared memory a 128 x 128 x 16 product reads 8 KB in the 64 cycles that the
+// tensor core needs for it, the whole bandwidth, and took 90 to 100 cycles.
 #include "lbsa_device.cuh"
 
 namespace lbsa {
@@ -33,7 +37,7 @@ constexpr int BM = 128;             // rows of a tile, columns of a step
 #define LBSA_GRAD_GROUPS 4
 #endif
 #ifndef LBSA_GRAD_POLY8
-#define LBSA_GRAD_POLY8 0
+#define LBSA_GRAD_POLY8 4
 #endif
 constexpr int kGroups = LBSA_GRAD_GROUPS;        // softmax warpgroups, kCols columns of a step each
 constexpr int kCols = BM / kGroups;
@@ -42,7 +46,8 @@ constexpr int kProducer = kGroups * 4, kIssuer = kProducer + 1;     // their war
 constexpr int kThreads = (kIssuer + 1) * 32;
 constexpr int N1 = 3, N2 = 2;       // ring depths of the two operands
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kS = 0, kDP = 128, kAcc1 = 256, kAcc2 = 384, kDS = 384;
+constexpr uint32_t kS = 0, kDP = 128, kAcc1 = 256, kAcc2 = 384;
+constexpr uint32_t kRows1 = 384, kRows2 = 448;      // queries: the tile's q and dout, two bf16 a column
 
 template <int D>
 struct Layout {
@@ -51,17 +56,19 @@ struct Layout {
   static constexpr int OFF_C1 = 2 * TILE, OFF_C2 = OFF_C1 + N1 * TILE;
   static constexpr int OFF_COL = OFF_C2 + N2 * TILE;         // per stage: 128 lse, 128 D
   static constexpr int OFF_BAR = OFF_COL + N2 * 2 * BM * 4;
-  static constexpr int OFF_MISC = OFF_BAR + 16 * 8;          // tmem, abort, count, pad, entries[N2][2]
-  static constexpr int BYTES = OFF_MISC + 64;
+  static constexpr int OFF_MISC = OFF_BAR + 18 * 8;          // tmem, abort, count, pad, entries[4][2]
+  static constexpr int BYTES = OFF_MISC + 48;
 };
 
+// c_empty: a step's last product is done (first operand's stage, columns' lse
+// and D); c2_empty: the second operand's last product is done.
 struct Bars {
-  uint64_t *r_full, *c1_full, *c2_full, *c_empty, *s_full, *dp_full, *drain, *s_done, *dp_done, *ds_full;
+  uint64_t *r_full, *c1_full, *c2_full, *col_full, *c_empty, *c2_empty, *s_full, *dp_full, *drain, *s_done, *ds_full;
 };
-constexpr int kBars = 15, kWarpBars = 11;      // from kWarpBars on every softmax warp arrives
+constexpr int kBars = 18, kWarpBars = 16;      // from kWarpBars on every softmax warp arrives
 __device__ __forceinline__ Bars make_bars(uint8_t* base) {
   uint64_t* b = reinterpret_cast<uint64_t*>(base);
-  return Bars{b, b + 1, b + 4, b + 6, b + 8, b + 9, b + 10, b + 11, b + 12, b + 13};
+  return Bars{b, b + 1, b + 4, b + 6, b + 8, b + 11, b + 13, b + 14, b + 15, b + 16, b + 17};
 }
 
 // Bulk copy of `bytes` (a multiple of 16) into shared memory, counted on `bar`.
@@ -132,47 +139,61 @@ __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const C
     for (int c = 0; c < D / 64; ++c) tma_load_4d(dst + c * BM * 128 + half * 64 * 128, m, bar, c * 64, piece * 64, t.h, t.b);
   };
   if (t.n_steps == 0) return;
-  mbar_arrive_expect_tx(bars.r_full, 2 * L::TILE);
-  for (int p = 0; p < 2; ++p) {
-    load(smem + L::OFF_R1, r1, bars.r_full, p, t.tile * 2 + p);
-    load(smem + L::OFF_R2, r2, bars.r_full, p, t.tile * 2 + p);
-  }
-  int j = 0, done1 = 0, done2 = 0;
-  for (; j < t.n_steps; ++j) {
-    uint32_t e[2];
-    e[0] = walk.next();
-    e[1] = walk.next();
-    if (e[1] == 0xFFFFFFFFu) e[1] = e[0] & 0x3FFFFFFFu;       // an odd tail: the piece again, kept by nobody
-    // stage j % 3 was freed by step j - 3, whose end was waited for below at step j - 1
-    uint8_t* s1 = smem + L::OFF_C1 + (j % N1) * L::TILE;
-    uint64_t* f1 = bars.c1_full + j % N1;
-    mbar_arrive_expect_tx(f1, L::TILE);
-    for (int p = 0; p < 2; ++p) load(s1, c1, f1, p, e[p] & 0x3FFFFFFFu);
-    done1 = j + 1;
-    if (j >= N2 && !mbar_wait(bars.c_empty + (j & 1), ((j >> 1) & 1) ^ 1, a.wait_limit, a.status, abort_flag)) break;
-    uint8_t* s2 = smem + L::OFF_C2 + (j & 1) * L::TILE;
-    uint64_t* f2 = bars.c2_full + (j & 1);
-    entries[(j & 1) * 2] = e[0];
-    entries[(j & 1) * 2 + 1] = e[1];
-    mbar_arrive_expect_tx(f2, L::TILE + (KEYS ? 2 * BM * 4 : 0));
+  if (KEYS) {
+    mbar_arrive_expect_tx(bars.r_full, 2 * L::TILE);
     for (int p = 0; p < 2; ++p) {
-      const int piece = e[p] & 0x3FFFFFFFu;
-      load(s2, c2, f2, p, piece);
-      if (KEYS) {
-        float* col = reinterpret_cast<float*>(smem + L::OFF_COL) + (j & 1) * 2 * BM + p * 64;
-        bulk_load(col, a.neg_lse2 + t.bh * a.Npad + piece * 64, 256, f2);
-        bulk_load(col + BM, a.neg_delta + t.bh * a.Npad + piece * 64, 256, f2);
-      }
+      load(smem + L::OFF_R1, r1, bars.r_full, p, t.tile * 2 + p);
+      load(smem + L::OFF_R2, r2, bars.r_full, p, t.tile * 2 + p);
     }
+  }
+  uint32_t e[2], ahead[2];          // pieces of this step, of the next one
+  int done1 = 0, done2 = 0, done_col = 0;
+  // step j's first operand into the stage that step j - 3 had
+  auto first = [&](int j, int stage) {
+    ahead[0] = walk.next();
+    ahead[1] = walk.next();
+    if (ahead[1] == 0xFFFFFFFFu) ahead[1] = ahead[0] & 0x3FFFFFFFu;       // an odd tail: the piece again, kept by nobody
+    entries[(j & 3) * 2] = ahead[0];
+    entries[(j & 3) * 2 + 1] = ahead[1];
+    mbar_arrive_expect_tx(bars.c1_full + stage, L::TILE);
+    for (int p = 0; p < 2; ++p) load(smem + L::OFF_C1 + stage * L::TILE, c1, bars.c1_full + stage, p, ahead[p] & 0x3FFFFFFFu);
+    done1 = j + 1;
+  };
+  first(0, 0);
+  int stage = 1;                    // of step j + 1
+  for (int j = 0; j < t.n_steps; ++j) {
+    e[0] = ahead[0];
+    e[1] = ahead[1];
+    if (j >= N2 && !mbar_wait(bars.c2_empty + (j & 1), ((j >> 1) & 1) ^ 1, a.wait_limit, a.status, abort_flag)) break;
+    uint64_t* f2 = bars.c2_full + (j & 1);
+    mbar_arrive_expect_tx(f2, L::TILE);
+    for (int p = 0; p < 2; ++p) load(smem + L::OFF_C2 + (j & 1) * L::TILE, c2, f2, p, e[p] & 0x3FFFFFFFu);
     done2 = j + 1;
+    // step j - 2 is over: its columns' values and the stage that step j + 1 takes are free
+    if (j >= 2 && !mbar_wait(bars.c_empty + stage, (((j - 2) / N1) & 1), a.wait_limit, a.status, abort_flag)) break;
+    if (KEYS) {
+      uint64_t* fc = bars.col_full + (j & 1);
+      mbar_arrive_expect_tx(fc, 2 * BM * 4);
+      for (int p = 0; p < 2; ++p) {
+        const int piece = e[p] & 0x3FFFFFFFu;
+        float* col = reinterpret_cast<float*>(smem + L::OFF_COL) + (j & 1) * 2 * BM + p * 64;
+        bulk_load(col, a.neg_lse2 + t.bh * a.Npad + piece * 64, 256, fc);
+        bulk_load(col + BM, a.neg_delta + t.bh * a.Npad + piece * 64, 256, fc);
+      }
+      done_col = j + 1;
+    }
+    if (j + 1 < t.n_steps) first(j + 1, stage);
+    if (++stage == N1) stage = 0;
   }
   if (*abort_flag) {
     // copies still in flight land before the CTA can exit
-    mbar_wait(bars.r_full, 0, a.wait_limit, a.status, nullptr);
+    if (KEYS) mbar_wait(bars.r_full, 0, a.wait_limit, a.status, nullptr);
     for (int s = max(done1 - N1, 0); s < done1; ++s)
       mbar_wait(bars.c1_full + s % N1, (s / N1) & 1, a.wait_limit, a.status, nullptr);
     for (int s = max(done2 - N2, 0); s < done2; ++s)
       mbar_wait(bars.c2_full + s % N2, (s / N2) & 1, a.wait_limit, a.status, nullptr);
+    for (int s = max(done_col - N2, 0); s < done_col; ++s)
+      mbar_wait(bars.col_full + s % N2, (s / N2) & 1, a.wait_limit, a.status, nullptr);
   }
 }
 
@@ -184,6 +205,13 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint64_t x, uint64_t y) {
     const uint64_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
     umma_ss(d, x + off, y + off, idesc_bf16_f32(BM, BM, 0), kk > 0 ? 1u : 0u);
   }
+}
+// the same with x's rows packed in TMEM
+template <int D>
+__device__ __forceinline__ void mma_rows_ts(uint32_t d, uint32_t x, uint64_t y) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    umma_ts(d, x + kk * 8, y + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4), idesc_bf16_f32(BM, BM, 0), kk > 0 ? 1u : 0u);
 }
 // d[128 x D] += p y; p packed in TMEM (each warpgroup's kCols columns start `pitch` further), y: MN-major rows
 template <int D>
@@ -199,10 +227,10 @@ __device__ __forceinline__ void mma_sum(uint32_t d, uint32_t p, uint32_t pitch, 
 // warp-uniform, and one elected lane issues: with a single lane in the loop the
 // operands went through per-thread registers and an instruction took about 100
 // cycles to issue, where the tensor core needs 64 for it.
-// ds_full is a pair: dP of step j + 1 is issued before dS of step j is waited
-// for (queries), so the softmax warps may finish step j + 1's dS first, and on
-// one barrier the phase of step j would then be missed.  Every other barrier's
-// next phase needs an instruction that follows the wait for the last one.
+// c_empty is a ring of three: the producer loads step j's second operand before
+// it waits for the end of step j - 2, so that on a pair step j's end could come
+// first and the phase be missed.  Every other barrier's next phase needs an
+// instruction that follows the wait for the last one.
 // tcgen05.mma instructions of one thread complete in the order of their issue:
 // S of step j + 1 may follow the product that reads P of step j from the same
 // columns, and dP the one that reads dS.
@@ -223,7 +251,8 @@ __device__ __forceinline__ void issue(uint8_t* smem, const Bars& bars, uint32_t 
   auto s_of = [&](int) {
     if (!wait(bars.c1_full + st_next, ph_next)) return false;
     if (elect_one()) {
-      mma_rows<D>(tmem + kS, r1, c1 + st_next * STAGE);
+      if (KEYS) mma_rows<D>(tmem + kS, r1, c1 + st_next * STAGE);
+      else mma_rows_ts<D>(tmem + kS, tmem + kRows1, c1 + st_next * STAGE);
       umma_commit(bars.s_full);
     }
     __syncwarp();
@@ -237,8 +266,10 @@ __device__ __forceinline__ void issue(uint8_t* smem, const Bars& bars, uint32_t 
   auto dp_of = [&](int j) {
     if (!wait(bars.c2_full + (j & 1), (j >> 1) & 1)) return false;
     if (elect_one()) {
-      mma_rows<D>(tmem + kDP, r2, c2 + (j & 1) * STAGE);
+      if (KEYS) mma_rows<D>(tmem + kDP, r2, c2 + (j & 1) * STAGE);
+      else mma_rows_ts<D>(tmem + kDP, tmem + kRows2, c2 + (j & 1) * STAGE);
       umma_commit(bars.dp_full);
+      if (!KEYS) umma_commit(bars.c2_empty + (j & 1));
     }
     __syncwarp();
     return true;
@@ -249,22 +280,20 @@ __device__ __forceinline__ void issue(uint8_t* smem, const Bars& bars, uint32_t 
     const int mine = st;                        // step j's stage of the first operand
     if (!wait(bars.s_done, j & 1)) break;
     if (KEYS) {
-      if (elect_one()) mma_sum<D>(tmem + kAcc2, tmem + kS, kCols, m2 + (j & 1) * STAGE, j == 0);
+      if (elect_one()) {
+        mma_sum<D>(tmem + kAcc2, tmem + kS, kCols, m2 + (j & 1) * STAGE, j == 0);
+        umma_commit(bars.c2_empty + (j & 1));
+      }
       __syncwarp();
     }
     if (more && !s_of(j + 1)) break;
-    if (!KEYS) {
-      if (!wait(bars.dp_done, j & 1)) break;
-      if (more && !dp_of(j + 1)) break;
-    }
-    if (!wait(bars.ds_full + (j & 1), (j >> 1) & 1)) break;
+    if (!wait(bars.ds_full, j & 1)) break;
     if (elect_one()) {
-      if (KEYS) mma_sum<D>(tmem + kAcc1, tmem + kDP, kCols, m1 + mine * STAGE, j == 0);
-      else mma_sum<D>(tmem + kAcc1, tmem + kDS + (j & 1) * 64, kCols / 2, m1 + mine * STAGE, j == 0);
-      umma_commit(bars.c_empty + (j & 1));
+      mma_sum<D>(tmem + kAcc1, tmem + kDP, kCols, m1 + mine * STAGE, j == 0);
+      umma_commit(bars.c_empty + mine);
     }
     __syncwarp();
-    if (KEYS && more && !dp_of(j + 1)) break;
+    if (more && !dp_of(j + 1)) break;
   }
   // every UMMA has completed before the sums are read and TMEM is released
   if (elect_one()) umma_commit(bars.drain);
@@ -337,15 +366,41 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
   const uint32_t s_col = t_lane + kS + c0, dp_col = t_lane + kDP + c0;
   const long long wl = a.wait_limit;
   float neg_lse = 0.f, neg_delta = 0.f;
-  if (!KEYS) {
+  if (!KEYS && t.n_steps > 0) {
     neg_lse = a.neg_lse2[t.bh * a.Npad + grow];
     neg_delta = a.neg_delta[t.bh * a.Npad + grow];
+    // the tile's own rows into TMEM: each warpgroup a part of q's or dout's row
+    constexpr int PART = 4 / kGroups * D / 4;      // 32-bit words
+    const GradStride& st = a.st[wg & 1 ? kDout : kQ];
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(wg & 1 ? a.dout : a.q) + t.b * st.b +
+                                                      t.h * st.h + grow * st.n) + (wg >> 1) * (PART / 4);
+    const uint32_t dst = t_lane + (wg & 1 ? kRows2 : kRows1) + (wg >> 1) * PART;
+#pragma unroll
+    for (int c = 0; c < PART; c += 16) {
+      uint32_t v[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = grow < a.N_valid ? __ldg(src + c / 4 + i) : make_uint4(0u, 0u, 0u, 0u);
+        v[4 * i] = x.x;
+        v[4 * i + 1] = x.y;
+        v[4 * i + 2] = x.z;
+        v[4 * i + 3] = x.w;
+      }
+      tmem_st16(dst + c, v);
+    }
+    tmem_wait_st();
+    warp_arrive(bars.r_full, lane);
   }
   bool alive = true;
+  int stage = 0, phase = 0;         // of the first operand's ring
   for (int j = 0; j < t.n_steps; ++j) {
-    alive = warp_wait(bars.c2_full + (j & 1), (j >> 1) & 1, wl, a.status, abort_flag);
+    alive = warp_wait(bars.c1_full + stage, phase, wl, a.status, abort_flag);
     if (!alive) break;
-    const uint32_t e = entries[(j & 1) * 2 + p];
+    if (++stage == N1) {
+      stage = 0;
+      phase ^= 1;
+    }
+    const uint32_t e = entries[(j & 3) * 2 + p];
     const int piece = e & 0x3FFFFFFFu;
     const bool take = (e >> (30 + half)) & 1u;                       // the same for the warp
     // the thread's columns that count, as bits from bit 0
@@ -361,6 +416,10 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
     if (!take) on = 0ull;
     const bool all = !MASKED && take && (KEYS || a.N_valid - piece * 64 - in_piece >= CPT);   // the same for the warp
     const float* col = reinterpret_cast<const float*>(smem + L::OFF_COL) + (j & 1) * 2 * BM + c0;
+    if (KEYS) {
+      alive = warp_wait(bars.col_full + (j & 1), (j >> 1) & 1, wl, a.status, abort_flag);
+      if (!alive) break;
+    }
     alive = warp_wait(bars.s_full, j & 1, wl, a.status, abort_flag);
     if (!alive) break;
     tc_fence_after();
@@ -380,15 +439,14 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
     if (!alive) break;
     tc_fence_after();
     load_cols<CPT>(dp_col, g);
-    if (!KEYS) warp_arrive(bars.dp_done, lane);                      // the dP columns are free
     score_gradients<CPT, KEYS>(g, r, col + BM, neg_delta);
     if (!all) {
       // a pair that is not kept gets 0, whatever its dP holds
 #pragma unroll
       for (int c = 0; c < CPT; ++c) g[c] = ((on >> c) & 1ull) ? g[c] : 0u;
     }
-    store_packed<CPT>(KEYS ? dp_col : t_lane + kDS + (j & 1) * 64 + wg * (CPT / 2), g);
-    warp_arrive(bars.ds_full + (j & 1), lane);
+    store_packed<CPT>(dp_col, g);
+    warp_arrive(bars.ds_full, lane);
   }
   // ---- the rows' sums
   bool sums = alive && t.n_steps > 0;
@@ -438,7 +496,7 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
   uint32_t* entries = misc + 4;
   if (threadIdx.x == 0) {
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-    for (int i = 0; i < kBars; ++i) mbar_init(b + i, i >= kWarpBars ? kGroups * 4 : 1);
+    for (int i = 0; i < kBars; ++i) mbar_init(b + i, i >= kWarpBars || (i == 0 && !KEYS) ? kGroups * 4 : 1);   // r_full is barrier 0
     misc[1] = 0;
     misc[2] = 0;
     fence_barrier_init();

@@ -677,7 +677,7 @@ int lbsa_attend_backward(const void* q, const void* k, const void* v, const void
   if (dev != bs->device) return fail(LBSA_ERR_INVALID_ARG, "blockset lives on device %d, current is %d", bs->device, dev);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   lbsa::AttendGradArgs a{desc->B, desc->H, desc->N_valid, desc->d, bs->block, bs->nB, bs->counts, bs->cols, bs->masks,
-                         bs->status, dq, dk, dv, {}, wait_limit()};
+                         bs->status, q, dout, dq, dk, dv, {}, wait_limit()};
   for (int i = 0; i < lbsa::kGradTensors; ++i) a.st[i] = st[i];
   DeviceState* ds = nullptr;
   Scratch ws;

@@ -156,6 +156,7 @@ struct AttendGradArgs {
   const int32_t* cols;
   const uint64_t* masks;        // per-token scope, as AttendArgs::masks
   int32_t* status;
+  const void *q, *dout;         // a query tile's own rows are read without a tensor map
   void *dq, *dk, *dv;
   GradStride st[kGradTensors];
   long long wait_limit;
