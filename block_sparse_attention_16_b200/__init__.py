@@ -26,6 +26,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -97,8 +98,7 @@ def load_library():
         "lbsa_select_rule": (ctypes.c_int, [P, I32, I32, I32, I32, I32, I32, D, I32, ctypes.POINTER(P), P]),
         "lbsa_score_attend": (ctypes.c_int, [P, P, P, ctypes.POINTER(_Desc), I32, P, P, P, P]),
         "lbsa_attend": (ctypes.c_int, [P, P, P, ctypes.POINTER(_Desc), P, P, P, P]),
-        "lbsa_attend_backward": (ctypes.c_int, [P, P, P, P, P, P, ctypes.POINTER(_Desc), ctypes.POINTER(I64),
-                                                P, P, P, P, P]),
+        "lbsa_attend_backward": (ctypes.c_int, [P, P, P, P, P, P, ctypes.POINTER(_Desc), P, P, P, P, P, P]),
         "lbsa_free": (None, [P]),
         "lbsa_blockset_info": (ctypes.c_int, [P] + [ctypes.POINTER(I32)] * 5),
         "lbsa_blockset_views": (ctypes.c_int, [P, ctypes.POINTER(P), ctypes.POINTER(P)]),
@@ -115,12 +115,10 @@ def load_library():
         "lbsa_permute": (ctypes.c_int, [ctypes.POINTER(P), ctypes.POINTER(P), I32, P,
                                         ctypes.POINTER(_Desc), I32, P]),
         "lbsa_rope_table": (ctypes.c_int, [ctypes.POINTER(I32), ctypes.POINTER(I32), D, ctypes.POINTER(D), P, P]),
-        "lbsa_rope": (ctypes.c_int, [ctypes.POINTER(_RopeItem), I32, I32, I32, I32, I32,
-                                     ctypes.POINTER(_RopePos), P, I32, P]),
-        "lbsa_norm_rope": (ctypes.c_int, [ctypes.POINTER(_RopeItem), I32, I32, I32, I32, I32,
-                                          ctypes.POINTER(_RopePos), P, D, P]),
-        "lbsa_norm_rope_backward": (ctypes.c_int, [ctypes.POINTER(_RopeItem), I32, I32, I32, I32, I32,
-                                                   ctypes.POINTER(_RopePos), P, D, P]),
+        # items and pos: _RopeItem arrays and _RopePos, or their bytes
+        "lbsa_rope": (ctypes.c_int, [P, I32, I32, I32, I32, I32, P, P, I32, P]),
+        "lbsa_norm_rope": (ctypes.c_int, [P, I32, I32, I32, I32, I32, P, P, D, P]),
+        "lbsa_norm_rope_backward": (ctypes.c_int, [P, I32, I32, I32, I32, I32, P, P, D, P]),
         "lbsa_selftest_wait": (ctypes.c_int, [I64, P, P]),
         "lbsa_selftest_exp2": (ctypes.c_int, [P, P, I64, P]),
         "lbsa_select_head_noalloc": (ctypes.c_int, [P, I32, I32, I32, D, P, P, P, P]),
@@ -142,8 +140,8 @@ def _check(rc: int):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _ptr(t):
@@ -370,6 +368,9 @@ def lbsa_attend(q, k, v, bs: Blockset, out=None, lse=None, want_lse=False, strea
     return (out, lse) if (want_lse or lse is not None) else out
 
 
+_PACK_STRIDES = struct.Struct("24q").pack
+
+
 def lbsa_attend_backward(q, k, v, bs: Blockset, out, lse, dout, dq=None, dk=None, dv=None, stream=None):
     """Gradients (dq, dk, dv) of lbsa_attend over bs, from its out and lse
     (want_lse=True) and the gradient dout of out.  The tensors share q's shape
@@ -378,21 +379,23 @@ def lbsa_attend_backward(q, k, v, bs: Blockset, out, lse, dout, dq=None, dk=None
     desc = _desc(q)
     dq, dk, dv = (torch.empty_like(x) if t is None else t for x, t in ((q, dq), (k, dk), (v, dv)))
     tensors = (q, k, v, out, dout, dq, dk, dv)
-    strides = (ctypes.c_int64 * 24)()
-    for i, t in enumerate(tensors):
-        if t.shape != q.shape or t.dtype != q.dtype or t.device != q.device or t.stride(3) != 1:
+    shape, dtype, device = q.shape, q.dtype, q.get_device()
+    B, H, N, d = shape
+    strides = []
+    for t in tensors:
+        st = t.stride()
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != device or st[3] != 1:
             raise LbsaError(LBSA_ERR_INVALID_ARG, "q, k, v, out, dout and the gradients must share shape, dtype and "
                                                   "device, with a contiguous last dim")
-        for j, (st, size) in enumerate(zip(t.stride()[:3], t.shape)):
-            strides[3 * i + j] = st if size > 1 else q.shape[3]
-    B, H, N, _ = q.shape
+        # the stride of a dimension of one entry means nothing
+        strides += st[:3] if B > 1 and H > 1 and N > 1 else [a if size > 1 else d for a, size in zip(st, shape)][:3]
     if lse is None:
         raise LbsaError(LBSA_ERR_INVALID_ARG, "lse is needed (lbsa_attend with want_lse=True)")
     _on_device(lse, "lse", torch.float32, B * H * N)
     desc.stride_b, desc.stride_h, desc.stride_n = strides[0:3]
-    _check(load_library().lbsa_attend_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse),
-                                               ctypes.byref(desc), strides, bs.handle, _ptr(dq), _ptr(dk), _ptr(dv),
-                                               _stream(stream)))
+    _check(load_library().lbsa_attend_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
+                                               lse.data_ptr(), ctypes.byref(desc), _PACK_STRIDES(*strides), bs.handle,
+                                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _stream(stream)))
     return dq, dk, dv
 
 
@@ -541,51 +544,66 @@ def lbsa_rope_table(grid, dims, theta: float = 10000.0, start=(0.0, 0.0, 0.0), t
     return table
 
 
+_PACK_ITEM = struct.Struct("5Q4i9q").pack          # _RopeItem
+_PACK_POS = struct.Struct("Q8i").pack               # _RopePos
+assert struct.calcsize("5Q4i9q") == ctypes.sizeof(_RopeItem) and struct.calcsize("Q8i") == ctypes.sizeof(_RopePos)
+
+
 def _rope_call(xs, ys, dys, weights, dweights, table, grid, dims, layout, perm):
     """The arguments that lbsa_rope, lbsa_norm_rope and lbsa_norm_rope_backward share."""
     n = len(xs)
     if not 1 <= n <= 3 or len(ys) != n or len(weights) != n or (dys is not None and len(dys) != n):
         raise LbsaError(LBSA_ERR_INVALID_ARG, "need 1..3 tensors, with as many weights (None: no norm), outputs and gradients")
-    items = (_RopeItem * n)()
     first = xs[0]
     if first.dim() != 4:
         raise LbsaError(LBSA_ERR_INVALID_ARG, "expected [B, H, N, d] tensors")
     B, _, N, d = first.shape
+    dtype = first.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise LbsaError(LBSA_ERR_UNSUPPORTED, f"dtype {dtype}")
+    _on_device(first, "x", contiguous=False)
+    device = first.get_device()
+    packed = b""
     for i, x in enumerate(xs):
-        if x.dtype not in (torch.bfloat16, torch.float32):
-            raise LbsaError(LBSA_ERR_UNSUPPORTED, f"dtype {x.dtype}")
-        if x.dim() != 4 or (x.shape[0], x.shape[2], x.shape[3], x.dtype) != (B, N, d, first.dtype):
+        shape = x.shape
+        H = shape[1]
+        if len(shape) != 4 or shape[0] != B or shape[2] != N or shape[3] != d:
             raise LbsaError(LBSA_ERR_INVALID_ARG, "tensors of one call must share B, N, d and dtype")
-        it, group = items[i], {"x": x, "y": ys[i]}
-        if dys is not None:
-            group["dy"] = dys[i]
-        for name, t in group.items():
-            _on_device(t, name, x.dtype, contiguous=False)
-            if t.shape != x.shape or t.stride(-1) != 1:
-                raise LbsaError(LBSA_ERR_INVALID_ARG, f"{name} must have x's shape and a contiguous last dim")
-            setattr(it, name, t.data_ptr())
-            setattr(it, name + "_stride", (ctypes.c_int64 * 3)(*(st if size > 1 else d for st, size in
-                                                                  zip(t.stride()[:3], t.shape[:3]))))
-        it.H, it.rotate = x.shape[1], int(weights[i] is not None or dweights is None)
-        w = weights[i]
-        if w is None:
-            continue
-        _on_device(w, "weight")
-        if w.dtype not in (torch.bfloat16, torch.float32) or w.shape not in ((d,), (x.shape[1], d)):
-            raise LbsaError(LBSA_ERR_INVALID_ARG, "a weight is bf16 or fp32, [d] or [H, d]")
-        it.weight, it.weight_dtype = w.data_ptr(), 0 if w.dtype == torch.bfloat16 else 1
-        it.weight_heads = 1 if w.dim() == 1 else x.shape[1]
-        if dweights:
-            it.dweight = dweights[i].data_ptr()
+        strides = []
+        for t in ((x, ys[i]) if dys is None else (x, ys[i], dys[i])):
+            if t.get_device() != device or t.dtype is not dtype:
+                _on_device(t, "a tensor of the call", dtype, contiguous=False)
+            st = t.stride()
+            if t.shape != shape or st[3] != 1:
+                raise LbsaError(LBSA_ERR_INVALID_ARG, "tensors of one call must share B, N, d and dtype, outputs and "
+                                                      "gradients their input's shape, with a contiguous last dim")
+            # the stride of a dimension of one entry means nothing
+            strides += st[:3] if B > 1 and H > 1 and N > 1 else [a if size > 1 else d for a, size in zip(st, shape)][:3]
+        if dys is None:
+            strides += (d, d, d)
+        w, wp, dwp, wt, wh = weights[i], 0, 0, 0, 1
+        if w is not None:
+            if w.get_device() != device or not w.is_contiguous():
+                _on_device(w, "weight")
+            if w.dtype not in (torch.bfloat16, torch.float32) or w.shape not in ((d,), (H, d)):
+                raise LbsaError(LBSA_ERR_INVALID_ARG, "a weight is bf16 or fp32, [d] or [H, d]")
+            wp, wt = w.data_ptr(), 0 if w.dtype is torch.bfloat16 else 1
+            wh = 1 if w.dim() == 1 else H
+            dwp = dweights[i].data_ptr() if dweights else 0
+        packed += _PACK_ITEM(x.data_ptr(), ys[i].data_ptr(), 0 if dys is None else dys[i].data_ptr(), wp, dwp, H,
+                             w is not None or dweights is None, wt, wh, *strides)
     pos = None
     if table is not None:
         if grid is None or dims is None or layout not in _ROPE_LAYOUTS:
             raise LbsaError(LBSA_ERR_INVALID_ARG, 'a rotation needs grid, dims and layout "interleaved" or "half"')
-        g, m = _three(grid, "grid", ctypes.c_int32), _three(dims, "dims", ctypes.c_int32)
-        _on_device(table, "table", torch.float32, max(sum(e * r for e, r in zip(g, m)), 0))
-        pos = ctypes.byref(_RopePos(table.data_ptr(), g, m, _ROPE_LAYOUTS[layout], 0))
-    _on_device(perm, "perm", torch.int32, N)
-    return items, n, B, N, d, 0 if first.dtype == torch.bfloat16 else 1, pos, _ptr(perm)
+        if len(grid) != 3 or len(dims) != 3:
+            raise LbsaError(LBSA_ERR_INVALID_ARG, "grid and dims must have three entries (time, height, width)")
+        _on_device(table, "table", torch.float32, max(sum(e * r for e, r in zip(grid, dims)), 0))
+        pos = _PACK_POS(table.data_ptr(), *grid, *dims, _ROPE_LAYOUTS[layout], 0)
+    if perm is not None:
+        _on_device(perm, "perm", torch.int32, N)
+        perm = perm.data_ptr()
+    return packed, n, B, N, d, 0 if dtype is torch.bfloat16 else 1, pos, perm
 
 
 def lbsa_rope(xs, table, grid, dims, perm=None, inverse: bool = False, layout: str = "interleaved", outs=None,

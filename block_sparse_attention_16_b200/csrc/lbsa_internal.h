@@ -194,8 +194,6 @@ struct RopePos {
   int half;                // pairs (i, i + rd/2) instead of (2i, 2i + 1)
   int tokens;              // T * Hg * Wg; later tokens are not rotated
 };
-// (batch, head chunk) units a call splits into: the grid's y extent
-int rope_units(const RopeItem* items, int count, int B, int N, bool backward);
 cudaError_t launch_rope(const RopeItem* items, int count, int B, int N, int d, int dtype, const RopePos& pos,
                         const int32_t* perm, float eps, int inverse, int32_t* status, cudaStream_t s);
 size_t norm_rope_backward_workspace_bytes(const RopeItem* items, int count, int B, int N, int d);

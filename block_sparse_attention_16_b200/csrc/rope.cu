@@ -15,22 +15,24 @@
 //
 // What bounds it: memory.  Every element is read once and written once
 // (backward: x and dy read, dx written).  A row is held by d / 8 lanes, eight
-// elements each, so the row sums are three or four shuffles; a thread takes
-// kHeads heads of one token, so their loads are in flight together and the
-// token's position, perm entry and (cos, sin) are looked up once for them.
+// elements each, so the row sums are three or four shuffles.  A block walks
+// token tiles of one unit (up to kMaxHeads heads of one tensor and batch
+// element): a token's position, perm entry and (cos, sin) are looked up once
+// for its heads, the weight once for the block, and the next rows' loads are in
+// flight while a batch of rows is worked on.
 #include "lbsa_device.cuh"
 
 namespace lbsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;        // heads of one token that a thread has in flight
+constexpr int kMaxHeads = 16;    // heads of a unit
 
 struct RopeArgs {
   RopeItem it[3];
   int count;
   int chunk_end[3];              // running number of (batch, head chunk) units per item
-  int heads[3];                  // heads of a unit (1 .. kHeads)
+  int heads[3];                  // heads of a unit (1 .. kMaxHeads)
   int N, d;
   RopePos pos;
   const int32_t* perm;
@@ -83,7 +85,7 @@ struct Eight<float> {
   }
 };
 
-// A lane's share of the rotation: which table entries its pairs take.
+// A lane's share of the rotation.
 // interleaved: pairs 4 l .. 4 l + 3 lie in the lane's own eight elements.
 // half-split: element e of the first half pairs with e + rd / 2, which a lane
 // rd / 16 further holds; both lanes look the pair's eight entries up.
@@ -91,41 +93,23 @@ template <bool HALF>
 struct Turn {
   static constexpr int P = HALF ? 8 : 4;
   float c[P], s[P];
-  int entry[P];       // table entry at position 0 of the pair's axis; -1: not rotated
-  int step[P];        // entries from one position to the next, axis in the low two bits
-  __device__ __forceinline__ void plan(const RopePos& pos, int lane, bool rotate) {
-    const int ht = pos.dt >> 1, hh = pos.dh >> 1, hw = pos.dw >> 1;
-    const int half = ht + hh + hw;
+  // token: source (raster) index; tokens past the grid and pairs past rd / 2 keep their place
+  __device__ __forceinline__ void look(const RopePos& pos, int lane, int token, float sign) {
+    const int ht = pos.dt >> 1, hh = pos.dh >> 1, hw = pos.dw >> 1, half = ht + hh + hw;
     const int first = HALF ? (lane * 8 < half ? lane * 8 : lane * 8 - half) : lane * 4;
+    const bool in = token < pos.tokens;
+    const uint32_t area = static_cast<uint32_t>(pos.Hg) * pos.Wg;
+    const uint32_t tok = static_cast<uint32_t>(in ? token : 0);
+    const uint32_t t = tok / area, r = tok - t * area, h = r / pos.Wg, w = r - h * pos.Wg;
+    // pair p of an axis: its table row's start plus p's place in the axis
+    const int row_t = static_cast<int>(t) * ht;
+    const int row_h = pos.T * ht + static_cast<int>(h) * hh - ht;
+    const int row_w = pos.T * ht + pos.Hg * hh + static_cast<int>(w) * hw - ht - hh;
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       const int p = first + j;
-      if (!rotate || p >= half) {
-        entry[j] = -1;
-        step[j] = 0;
-      } else if (p < ht) {
-        entry[j] = p;
-        step[j] = ht << 2;
-      } else if (p < ht + hh) {
-        entry[j] = pos.T * ht + p - ht;
-        step[j] = (hh << 2) | 1;
-      } else {
-        entry[j] = pos.T * ht + pos.Hg * hh + p - ht - hh;
-        step[j] = (hw << 2) | 2;
-      }
-    }
-  }
-  // token: source (raster) index; tokens past the grid keep their place
-  __device__ __forceinline__ void look(const RopePos& pos, int token, float sign) {
-    const bool in = token < pos.tokens;
-    const uint32_t area = static_cast<uint32_t>(pos.Hg) * pos.Wg;
-    const uint32_t tt = static_cast<uint32_t>(in ? token : 0);
-    const uint32_t t = tt / area, r = tt - t * area, h = r / pos.Wg, w = r - h * pos.Wg;
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const uint32_t at = (step[j] & 3) == 0 ? t : (step[j] & 3) == 1 ? h : w;
       float2 cs = make_float2(1.f, 0.f);
-      if (in && entry[j] >= 0) cs = __ldg(pos.table + entry[j] + static_cast<int>(at) * (step[j] >> 2));
+      if (in && p < half) cs = __ldg(pos.table + (p + (p < ht ? row_t : p < ht + hh ? row_h : row_w)));
       c[j] = cs.x;
       s[j] = cs.y * sign;
     }
@@ -154,19 +138,36 @@ struct Turn {
   }
 };
 
-template <int LANES>
-__device__ __forceinline__ float row_sum(float v) {
+// sums of the lanes of each row, n of them side by side
+template <int LANES, int n>
+__device__ __forceinline__ void row_sums(float (&v)[n]) {
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = LANES / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
 __device__ __forceinline__ void load_weight(const RopeItem& it, int head, int lane, int d, float (&w)[8]) {
   const long long at = static_cast<long long>(it.weight_heads > 1 ? head : 0) * d + lane * 8;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    w[j] = it.weight_dtype == LBSA_F32 ? __ldg(static_cast<const float*>(it.weight) + at + j)
-                                       : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(it.weight) + at + j));
+  if (it.weight_dtype == LBSA_F32) {
+    Eight<float> v;
+    v.load(static_cast<const float*>(it.weight) + at);
+    v.get(w);
+  } else {
+    Eight<__nv_bfloat16> v;
+    v.load(static_cast<const __nv_bfloat16*>(it.weight) + at);
+    v.get(w);
+  }
+}
+
+// The source token of a slot: -1 past the last slot, or for a bad perm entry
+// (reported by one lane).
+__device__ __forceinline__ int token_of(const RopeArgs& a, int slot, bool report) {
+  if (slot >= a.N) return -1;
+  const int tok = a.perm ? __ldg(a.perm + slot) : slot;
+  if (tok >= 0 && tok < a.N) return tok;
+  if (report) raise_status(a.status, LBSA_ERR_BAD_INDEX);
+  return -1;
 }
 
 struct Unit {
@@ -183,135 +184,224 @@ __device__ __forceinline__ Unit unit_of(const RopeArgs& a, int y) {
   return u;
 }
 
-// grid (token tiles, units): a block takes kThreads / LANES tokens at a time,
-// token tiles blockIdx.x, blockIdx.x + gridDim.x, ... of one unit.
+// grid (blocks along the tokens, units): a block takes kThreads / LANES tokens
+// at a time, token tiles blockIdx.x, blockIdx.x + gridDim.x, ... of one unit.
 template <typename T, int D, bool HALF>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
+  constexpr int kBatch = 8 / sizeof(T);          // heads of a token that a thread loads together: 64 bytes
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
   const Unit u = unit_of(a, blockIdx.y);
   const RopeItem& it = a.it[u.item];
   const T* x = static_cast<const T*>(it.x) + u.b * it.xs[0] + u.h0 * it.xs[1] + lane * 8;
   T* y = static_cast<T*>(it.y) + u.b * it.ys[0] + u.h0 * it.ys[1] + lane * 8;
+  const int64_t x_head = it.xs[1], y_head = it.ys[1];
+  const bool norm = it.weight != nullptr, rotate = it.rotate, per_head = norm && it.weight_heads > 1;
   Turn<HALF> turn;
-  turn.plan(a.pos, lane, it.rotate);
+  float w[8];
+  if (norm) load_weight(it, u.h0, lane, D, w);
   const float sign = a.inverse ? -1.f : 1.f;
-  const int tiles = (a.N + GROUPS - 1) / GROUPS;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int slot = tile * GROUPS + group;
-    int tok = slot < a.N ? (a.perm ? __ldg(a.perm + slot) : slot) : -1;
-    if (tok >= a.N || (tok < 0 && slot < a.N)) {
-      if (lane == 0) raise_status(a.status, LBSA_ERR_BAD_INDEX);
-      tok = -1;
-    }
-    const bool ok = tok >= 0;
-    const long long from = a.inverse ? slot : tok, to = a.inverse ? tok : slot;
-    Eight<T> v[kHeads];
+  const int tiles = (a.N + GROUPS - 1) / GROUPS, batches = (u.nh + kBatch - 1) / kBatch;
+
+  auto load = [&](Eight<T> (&v)[kBatch], int slot, int tok, int h) {
+    const T* row = x + static_cast<long long>(a.inverse ? slot : tok) * it.xs[2] + h * x_head;
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      if (ok && i < u.nh) v[i].load(x + from * it.xs[2] + i * it.xs[1]);
+    for (int i = 0; i < kBatch; ++i) {
+      if (tok >= 0 && h + i < u.nh) v[i].load(row + i * x_head);
       else v[i].zero();
     }
-    if (it.rotate) turn.look(a.pos, max(tok, 0), sign);
+  };
+  int slot = blockIdx.x * GROUPS + group, tok = token_of(a, slot, lane == 0);
+  Eight<T> cur[kBatch], nxt[kBatch];
+  load(cur, slot, tok, 0);
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int next_slot = slot + gridDim.x * GROUPS;
+    const int next_tok = tile + gridDim.x < tiles ? token_of(a, next_slot, lane == 0) : -1;
+    if (rotate) turn.look(a.pos, lane, max(tok, 0), sign);
+    T* out = y + static_cast<long long>(a.inverse ? tok : slot) * it.ys[2];
+    for (int b = 0; b < batches; ++b) {
+      const bool last = b + 1 == batches;
+      load(nxt, last ? next_slot : slot, last ? next_tok : tok, last ? 0 : (b + 1) * kBatch);
+      // the batch's row sums first, so that their shuffles overlap
+      float r[kBatch];
+      if (norm) {
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      if (i >= u.nh) break;                                    // the same for the whole block
-      float f[8];
-      v[i].get(f);
-      if (it.weight) {
-        float ss = 0.f;
+        for (int i = 0; i < kBatch; ++i) {
+          float f[8];
+          cur[i].get(f);
+          r[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
-        const float r = rsqrtf(row_sum<LANES>(ss) * (1.f / D) + a.eps);
-        float w[8];
-        load_weight(it, u.h0 + i, lane, D, w);
+          for (int j = 0; j < 8; ++j) r[i] = fmaf(f[j], f[j], r[i]);
+        }
+        row_sums<LANES>(r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] * r * w[j];
+        for (int i = 0; i < kBatch; ++i) r[i] = rsqrtf(r[i] * (1.f / D) + a.eps);
       }
-      if (it.rotate) turn.apply(f, a.pos, lane, LANES);
-      if (ok) {
-        T* dst = y + to * it.ys[2] + i * it.ys[1];
-        if (it.weight || it.rotate) Eight<T>::store(dst, f);
-        else v[i].copy_to(dst);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = b * kBatch + i;
+        float f[8];
+        cur[i].get(f);
+        if (norm) {
+          if (per_head) load_weight(it, u.h0 + min(h, u.nh - 1), lane, D, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = f[j] * r[i] * w[j];
+        }
+        if (rotate) turn.apply(f, a.pos, lane, LANES);
+        if (tok >= 0 && h < u.nh) {
+          if (norm || rotate) Eight<T>::store(out + h * y_head, f);
+          else cur[i].copy_to(out + h * y_head);
+        }
       }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) cur[i] = nxt[i];
     }
+    slot = next_slot;
+    tok = next_tok;
   }
 }
 
+// 16 bytes from global to shared memory, zeros where !on.
+__device__ __forceinline__ void async_16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
 // Same tiling; x is read in source order, dy in block order, dx written in
-// source order.  A thread adds its columns' du n over all its rows; the block
-// adds its groups' sums in a fixed order and writes one partial row, so the
-// weight gradient does not depend on the order in which blocks run.
+// source order.  A thread's rows come through its own slots of shared memory,
+// kStages - 1 batches ahead (no thread reads another's slots): with the next
+// batch in registers instead the kernel held 126 of them and took 168 us for a
+// layer's q, k, v (21 x 30 x 52 tokens, 12 heads of 128, bf16) where memory
+// needs 123.  A thread adds its columns' du n over all its rows; the block adds
+// its groups' sums in a fixed order and writes one partial row, so the weight
+// gradient does not depend on the order in which blocks run.
+constexpr int kStages = 4;
+constexpr int kStageVecs = 4;                    // 16-byte slots of a thread in a stage: 64 bytes of x and dy
+constexpr int kBackwardSmem = kStages * kStageVecs * kThreads * 16 + kThreads * 8 * 4;
+
 template <typename T, int D, bool HALF>
-__global__ void __launch_bounds__(kThreads) norm_rope_backward_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
-  __shared__ float sum[GROUPS][D];
+  constexpr int VECS = sizeof(T) / 2;            // slots of a row's eight elements
+  constexpr int kBatch = kStageVecs / (2 * VECS);
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint4* slots = reinterpret_cast<uint4*>(smem) + threadIdx.x;       // [stage][vec][thread]
+  float* sum = reinterpret_cast<float*>(smem + kStages * kStageVecs * kThreads * 16);   // [GROUPS][D]
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
   const Unit u = unit_of(a, blockIdx.y);
   const RopeItem& it = a.it[u.item];
-  const T* x = static_cast<const T*>(it.x) + u.b * it.xs[0] + u.h0 * it.xs[1] + lane * 8;
+  const bool norm = it.weight != nullptr, rotate = it.rotate;
+  // without a norm x is not read (it may be NULL)
+  const T* x = norm ? static_cast<const T*>(it.x) + u.b * it.xs[0] + u.h0 * it.xs[1] + lane * 8 : nullptr;
   const T* dy = static_cast<const T*>(it.dy) + u.b * it.ds[0] + u.h0 * it.ds[1] + lane * 8;
   T* dx = static_cast<T*>(it.y) + u.b * it.ys[0] + u.h0 * it.ys[1] + lane * 8;
   Turn<HALF> turn;
-  turn.plan(a.pos, lane, it.rotate);
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const int tiles = (a.N + GROUPS - 1) / GROUPS;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int slot = tile * GROUPS + group;
-    int tok = slot < a.N ? (a.perm ? __ldg(a.perm + slot) : slot) : -1;
-    if (tok >= a.N || (tok < 0 && slot < a.N)) {
-      if (lane == 0) raise_status(a.status, LBSA_ERR_BAD_INDEX);
-      tok = -1;
+  float w[8], acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (norm) load_weight(it, u.h0, lane, D, w);                 // a weight row for each head: one head a unit
+  const int tiles = (a.N + GROUPS - 1) / GROUPS, batches = (u.nh + kBatch - 1) / kBatch;
+  const int stride = gridDim.x;
+
+  // the batch to be fetched next: its tile, slot, token and head
+  int f_tile = blockIdx.x, f_slot = f_tile * GROUPS + group, f_tok = token_of(a, f_slot, lane == 0), f_h = 0, f_stage = 0;
+  int f_next = f_tile + stride < tiles ? token_of(a, f_slot + stride * GROUPS, false) : -1;
+  auto fetch = [&] {
+    const uint32_t dst = smem_u32(slots + f_stage * kStageVecs * kThreads);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const bool on = f_tok >= 0 && f_h + i < u.nh;
+      const T* rd = dy + (on ? f_slot * it.ds[2] + (f_h + i) * it.ds[1] : 0);
+      const T* rx = norm ? x + (on ? f_tok * it.xs[2] + (f_h + i) * it.xs[1] : 0) : rd;
+#pragma unroll
+      for (int v = 0; v < VECS; ++v) {
+        async_16(dst + (i * 2 * VECS + v) * kThreads * 16, reinterpret_cast<const uint4*>(rd) + v, on);
+        if (norm) async_16(dst + (i * 2 * VECS + VECS + v) * kThreads * 16, reinterpret_cast<const uint4*>(rx) + v, on);
+      }
     }
-    const bool ok = tok >= 0;
-    Eight<T> vx[kHeads], vd[kHeads];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      if (ok && i < u.nh) vd[i].load(dy + static_cast<long long>(slot) * it.ds[2] + i * it.ds[1]);
-      else vd[i].zero();
-      if (ok && i < u.nh && it.weight) vx[i].load(x + static_cast<long long>(tok) * it.xs[2] + i * it.xs[1]);
-      else vx[i].zero();
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++f_stage == kStages) f_stage = 0;
+    f_h += kBatch;
+    if (f_h >= u.nh) {
+      f_h = 0;
+      f_tile += stride;
+      f_slot += stride * GROUPS;
+      f_tok = f_next;
+      f_next = f_tile + stride < tiles ? token_of(a, f_slot + stride * GROUPS, false) : -1;
     }
-    if (it.rotate) turn.look(a.pos, max(tok, 0), -1.f);
+  };
+  auto take = [&](Eight<T>& v, int stage, int vec) {
+    uint4* to = reinterpret_cast<uint4*>(&v);
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      if (i >= u.nh) break;
-      float g[8];
-      vd[i].get(g);
-      if (it.rotate) turn.apply(g, a.pos, lane, LANES);
-      if (it.weight) {
-        float n[8], w[8], ss = 0.f;
-        vx[i].get(n);
-        load_weight(it, u.h0 + i, lane, D, w);
+    for (int i = 0; i < VECS; ++i) to[i] = slots[(stage * kStageVecs + vec + i) * kThreads];
+  };
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(n[j], n[j], ss);
-        const float r = rsqrtf(row_sum<LANES>(ss) * (1.f / D) + a.eps);
-        float dot = 0.f;
+  for (int i = 0; i < kStages - 1; ++i) fetch();
+
+  int slot = blockIdx.x * GROUPS + group, tok = token_of(a, slot, false), stage = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += stride) {
+    const int next_tok = tile + stride < tiles ? token_of(a, slot + stride * GROUPS, lane == 0) : -1;
+    if (rotate) turn.look(a.pos, lane, max(tok, 0), -1.f);
+    T* out = dx + static_cast<long long>(tok) * it.ys[2];
+    for (int b = 0; b < batches; ++b) {
+      fetch();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      Eight<T> cd[kBatch];
+      float g[kBatch][8], sums[2 * kBatch];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          n[j] *= r;
-          acc[j] = fmaf(g[j], n[j], acc[j]);
-          g[j] *= w[j];
-          dot = fmaf(g[j], n[j], dot);
+      for (int i = 0; i < kBatch; ++i) {
+        take(cd[i], stage, i * 2 * VECS);
+        cd[i].get(g[i]);
+        if (rotate) turn.apply(g[i], a.pos, lane, LANES);
+      }
+      if (norm) {
+        // sum x^2 and sum dn x of the batch together: mean(dn n) = r mean(dn x)
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          Eight<T> cx;
+          float n[8];
+          take(cx, stage, i * 2 * VECS + VECS);
+          cx.get(n);
+          sums[2 * i] = sums[2 * i + 1] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            sums[2 * i] = fmaf(n[j], n[j], sums[2 * i]);
+            sums[2 * i + 1] = fmaf(g[i][j] * w[j], n[j], sums[2 * i + 1]);
+          }
         }
-        dot = row_sum<LANES>(dot) * (1.f / D);
+        row_sums<LANES>(sums);
+      }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = r * (g[j] - n[j] * dot);
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = b * kBatch + i;
+        if (norm) {
+          Eight<T> cx;
+          float n[8];
+          take(cx, stage, i * 2 * VECS + VECS);
+          cx.get(n);
+          const float r = rsqrtf(sums[2 * i] * (1.f / D) + a.eps);
+          const float k = sums[2 * i + 1] * (1.f / D) * r * r;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            acc[j] = fmaf(g[i][j], n[j] * r, acc[j]);          // rows that are not there are 0
+            g[i][j] = r * fmaf(-n[j], k, g[i][j] * w[j]);
+          }
+        }
+        if (tok >= 0 && h < u.nh) {
+          if (norm || rotate) Eight<T>::store(out + h * it.ys[1], g[i]);
+          else cd[i].copy_to(out + h * it.ys[1]);
+        }
       }
-      if (ok) {
-        T* dst = dx + static_cast<long long>(tok) * it.ys[2] + i * it.ys[1];
-        if (it.weight || it.rotate) Eight<T>::store(dst, g);
-        else vd[i].copy_to(dst);
-      }
+      if (++stage == kStages) stage = 0;
     }
+    slot += stride * GROUPS;
+    tok = next_tok;
   }
-  if (!it.weight) return;
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (!norm) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) sum[group][lane * 8 + j] = acc[j];
+  for (int j = 0; j < 8; ++j) sum[group * D + lane * 8 + j] = acc[j];
   __syncthreads();
   for (int e = threadIdx.x; e < D; e += kThreads) {
     float t = 0.f;
-    for (int g = 0; g < GROUPS; ++g) t += sum[g][e];
+    for (int g = 0; g < GROUPS; ++g) t += sum[g * D + e];
     a.partial[(static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * D + e] = t;
   }
 }
@@ -328,13 +418,14 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const __grid_constant
   }
   const RopeItem& it = a.it[item];
   const int first = item ? a.chunk_end[item - 1] : 0;
-  const int per = (it.H + a.heads[item] - 1) / a.heads[item];
   const bool shared = it.weight_heads == 1;
-  const long long n = static_cast<long long>(shared ? a.chunk_end[item] - first : B) * gx;   // partial rows to add
+  // the units' partial rows lie together: all of the item's, or (one head a unit) one run a batch element
+  const long long run = shared ? static_cast<long long>(a.chunk_end[item] - first) * gx : gx;
   double t = 0.0;
-  for (long long i = threadIdx.y; i < n; i += 32) {
-    const long long unit = shared ? first + i / gx : first + (i / gx) * per + row;           // one head a unit there
-    t += a.partial[(unit * gx + i % gx) * a.d + e];
+  for (int b = 0; b < (shared ? 1 : B); ++b) {
+    const float* p = a.partial + static_cast<long long>(first + (shared ? 0 : b * it.H + row)) * gx * a.d + e;
+#pragma unroll 8
+    for (long long i = threadIdx.y; i < run; i += 32) t += __ldg(p + i * a.d);
   }
   sum[threadIdx.y][threadIdx.x] = t;
   __syncthreads();
@@ -362,29 +453,48 @@ __global__ void rope_table_kernel(RopePos p, double theta, double st, double sh,
   }
 }
 
-// Units: (batch, up to `heads` heads) of each item.  Few tokens: one head a
-// unit, so that a single token's heads run side by side.
-int plan_units(RopeArgs& a, const RopeItem* items, int count, int B, bool backward) {
-  int total = 0;
+int token_tiles(int N, int d) { return (N + kThreads / (d / 8) - 1) / (kThreads / (d / 8)); }
+
+// Units: (batch, up to `heads` heads) of each item.  With few tokens the heads
+// are spread over more units, down to one head, until four blocks an SM have
+// work: a single token's 24 heads of 128 take 4 us so, 6 us as two units.
+int plan_units(RopeArgs& a, const RopeItem* items, int count, int B, int N, int d, bool backward) {
   a.count = count;
-  for (int i = 0; i < 3; ++i) {
-    if (i < count) {
-      a.it[i] = items[i];
-      const bool own_rows = backward && items[i].weight && items[i].weight_heads > 1;
-      a.heads[i] = own_rows || static_cast<long long>(a.N) * B * items[i].H < 148ll * 64 ? 1 : std::min(items[i].H, kHeads);
-      total += B * ((items[i].H + a.heads[i] - 1) / a.heads[i]);
-    } else {
-      a.heads[i] = 1;
+  int total = 0;
+  for (int most = kMaxHeads; most >= 1; most /= 2) {
+    total = 0;
+    for (int i = 0; i < 3; ++i) {
+      if (i < count) {
+        a.it[i] = items[i];
+        const bool own_rows = backward && items[i].weight && items[i].weight_heads > 1;
+        a.heads[i] = own_rows ? 1 : std::min(items[i].H, most);
+        total += B * ((items[i].H + a.heads[i] - 1) / a.heads[i]);
+      } else {
+        a.heads[i] = 1;
+      }
+      a.chunk_end[i] = total;
     }
-    a.chunk_end[i] = total;
+    if (static_cast<long long>(total) * token_tiles(N, d) >= 148 * 4) break;
   }
   return total;
 }
 
+// Blocks along the tokens: about kBlocksPerSm an SM in all, so that a block
+// walks several tiles and the backward pass has few partial rows.
+constexpr int kBlocksPerSm = 9;
+int token_blocks(int N, int d, int units) {
+  return std::max(1, std::min(token_tiles(N, d), (148 * kBlocksPerSm + units - 1) / units));
+}
+
 template <bool BWD>
 cudaError_t launch(const RopeArgs& a, int dtype, dim3 grid, cudaStream_t s) {
+  const int smem = BWD ? kBackwardSmem : 0;
   auto go = [&](auto kern) {
-    kern<<<grid, kThreads, 0, s>>>(a);
+    if (BWD) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+    }
+    kern<<<grid, kThreads, smem, s>>>(a);
     return cudaGetLastError();
   };
 #define LBSA_ROPE(T, D)                                                                          \
@@ -395,21 +505,7 @@ cudaError_t launch(const RopeArgs& a, int dtype, dim3 grid, cudaStream_t s) {
 #undef LBSA_ROPE
 }
 
-int token_tiles(int N, int d) { return (N + kThreads / (d / 8) - 1) / (kThreads / (d / 8)); }
-
-// Blocks along the tokens in the backward pass: about eight blocks an SM in
-// all, so that the partial rows stay few.
-int backward_blocks(int N, int d, int units) {
-  return std::max(1, std::min(token_tiles(N, d), (148 * 8 + units - 1) / units));
-}
-
 }  // namespace
-
-int rope_units(const RopeItem* items, int count, int B, int N, bool backward) {
-  RopeArgs a{};
-  a.N = N;
-  return plan_units(a, items, count, B, backward);
-}
 
 cudaError_t launch_rope(const RopeItem* items, int count, int B, int N, int d, int dtype, const RopePos& pos,
                         const int32_t* perm, float eps, int inverse, int32_t* status, cudaStream_t s) {
@@ -421,13 +517,14 @@ cudaError_t launch_rope(const RopeItem* items, int count, int B, int N, int d, i
   a.eps = eps;
   a.inverse = inverse;
   a.status = status;
-  const int units = plan_units(a, items, count, B, false);
-  return launch<false>(a, dtype, dim3(token_tiles(N, d), units), s);
+  const int units = plan_units(a, items, count, B, N, d, false);
+  return launch<false>(a, dtype, dim3(token_blocks(N, d, units), units), s);
 }
 
 size_t norm_rope_backward_workspace_bytes(const RopeItem* items, int count, int B, int N, int d) {
-  const int units = rope_units(items, count, B, N, true);
-  return static_cast<size_t>(units) * backward_blocks(N, d, units) * d * sizeof(float);
+  RopeArgs a{};
+  const int units = plan_units(a, items, count, B, N, d, true);
+  return static_cast<size_t>(units) * token_blocks(N, d, units) * d * sizeof(float);
 }
 
 cudaError_t launch_norm_rope_backward(const RopeItem* items, int count, int B, int N, int d, int dtype,
@@ -441,8 +538,8 @@ cudaError_t launch_norm_rope_backward(const RopeItem* items, int count, int B, i
   a.eps = eps;
   a.status = status;
   a.partial = static_cast<float*>(workspace);
-  const int units = plan_units(a, items, count, B, true);
-  const int gx = backward_blocks(N, d, units);
+  const int units = plan_units(a, items, count, B, N, d, true);
+  const int gx = token_blocks(N, d, units);
   cudaError_t e = launch<true>(a, dtype, dim3(gx, units), s);
   int rows = 0;
   for (int i = 0; i < count; ++i) rows += items[i].weight ? items[i].weight_heads : 0;
