@@ -109,39 +109,42 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
 }
 
 // ------------------------------------------------------------------ CUDA cores
-// A CTA owns 64 rows (keys, or queries) and walks the 64-row pieces of the
+// A CTA owns R rows (keys, or queries) and walks the 64-row pieces of the
 // other side that its block is kept with.  256 threads as 16 x 16: thread
 // (ty, tx) computes S and dP for rows ty + 16 i and columns tx + 16 j, then,
-// P and dS in shared memory, its 4 rows x d / 16 columns of the sums.
+// P and dS in shared memory, its R / 16 rows x d / 16 columns of the sums.
+// Bound by shared-memory reads and FMA issue in about equal parts: at R = 64 a
+// thread reads 8 vectors for 64 FMAs.  R = 64 wherever that fills the SMs; with
+// fewer rows R = 32 or 16 spreads them over more CTAs (256 tokens, 2 heads of
+// 64, 60 % of the blocks: 55 us with R = 64).
 constexpr int kPitch = 68;        // floats a row of P and dS: 16-byte rows, no bank conflicts
 
 template <int D>
-__device__ __forceinline__ void load_piece(float* s, const float* g, long long stride, int r0, int N) {
-  for (int i = threadIdx.x; i < 64 * D / 2; i += 256) {
-    const int r = i / (D / 2), e = (i - r * (D / 2)) * 2;
-    float2 v = make_float2(0.f, 0.f);
-    if (r0 + r < N) v = load2<float>(g + (r0 + r) * stride + e);
-    *reinterpret_cast<float2*>(s + r * (D + 4) + e) = v;
+__device__ __forceinline__ void load_rows(float* s, const float* g, long long stride, int r0, int rows, int N) {
+  for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+    const int r = i / (D / 4), e = (i - r * (D / 4)) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + r < N) v = __ldg(reinterpret_cast<const float4*>(g + (r0 + r) * stride + e));
+    *reinterpret_cast<float4*>(s + r * (D + 4) + e) = v;
   }
 }
 
 // acc[i][j] = row ty + 16 i of x  .  row tx + 16 j of y
-template <int D>
-__device__ __forceinline__ void dots(float (&acc)[4][4], const float* x, const float* y, int ty, int tx) {
+template <int D, int RI>
+__device__ __forceinline__ void dots(float (&acc)[RI][4], const float* x, const float* y, int ty, int tx) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RI; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll 4
   for (int e = 0; e < D; e += 4) {
-    float4 xr[4], yr[4];
+    float4 xr[RI], yr[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      xr[i] = *reinterpret_cast<const float4*>(x + (ty + 16 * i) * (D + 4) + e);
-      yr[i] = *reinterpret_cast<const float4*>(y + (tx + 16 * i) * (D + 4) + e);
-    }
+    for (int i = 0; i < RI; ++i) xr[i] = *reinterpret_cast<const float4*>(x + (ty + 16 * i) * (D + 4) + e);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) yr[i] = *reinterpret_cast<const float4*>(y + (tx + 16 * i) * (D + 4) + e);
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         acc[i][j] = fmaf(xr[i].x, yr[j].x, fmaf(xr[i].y, yr[j].y, fmaf(xr[i].z, yr[j].z, fmaf(xr[i].w, yr[j].w, acc[i][j]))));
@@ -149,20 +152,20 @@ __device__ __forceinline__ void dots(float (&acc)[4][4], const float* x, const f
 }
 
 // acc[i][.] += sum_c w[ty + 16 i][c] y[c][columns of tx]
-template <int D>
-__device__ __forceinline__ void weighted(float (&acc)[4][D / 16], const float* w, const float* y, int ty, int tx) {
-#pragma unroll 2
+template <int D, int RI>
+__device__ __forceinline__ void weighted(float (&acc)[RI][D / 16], const float* w, const float* y, int ty, int tx) {
+#pragma unroll 4
   for (int c = 0; c < 64; c += 4) {
-    float4 wr[4];
+    float4 wr[RI];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wr[i] = *reinterpret_cast<const float4*>(w + (ty + 16 * i) * kPitch + c);
+    for (int i = 0; i < RI; ++i) wr[i] = *reinterpret_cast<const float4*>(w + (ty + 16 * i) * kPitch + c);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
       for (int g = 0; g < D / 64; ++g) {
         const float4 v = *reinterpret_cast<const float4*>(y + (c + k) * (D + 4) + g * 64 + tx * 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RI; ++i) {
           const float p = k == 0 ? wr[i].x : k == 1 ? wr[i].y : k == 2 ? wr[i].z : wr[i].w;
           acc[i][g * 4 + 0] = fmaf(p, v.x, acc[i][g * 4 + 0]);
           acc[i][g * 4 + 1] = fmaf(p, v.y, acc[i][g * 4 + 1]);
@@ -174,11 +177,11 @@ __device__ __forceinline__ void weighted(float (&acc)[4][D / 16], const float* w
   }
 }
 
-template <int D>
-__device__ __forceinline__ void store_rows(float* g, long long stride, int r0, int N, const float (&acc)[4][D / 16], float f,
-                                           int ty, int tx) {
+template <int D, int RI>
+__device__ __forceinline__ void store_rows(float* g, long long stride, int r0, int N, const float (&acc)[RI][D / 16],
+                                           float f, int ty, int tx) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RI; ++i) {
     const int r = r0 + ty + 16 * i;
     if (r >= N) continue;
 #pragma unroll
@@ -188,16 +191,20 @@ __device__ __forceinline__ void store_rows(float* g, long long stride, int r0, i
   }
 }
 
-// blockIdx.x: pieces of keys (dk, dv), then pieces of queries (dq).
-template <int D>
+template <int D, int R>
+constexpr int f32_smem() { return (2 * (R + 64) * (D + 4) + 2 * R * kPitch) * 4; }
+
+// blockIdx.x: tiles of keys (dk, dv), then tiles of queries (dq).
+template <int D, int R>
 __global__ void __launch_bounds__(256) attend_grad_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
                                                              const float* __restrict__ v, const float* __restrict__ dout,
-                                                             AttendGradArgs a, int pieces) {
-  extern __shared__ float sm[];
-  constexpr int PIECE = 64 * (D + 4);
-  float *r1 = sm, *r2 = r1 + PIECE, *c1 = r2 + PIECE, *c2 = c1 + PIECE, *sp = c2 + PIECE, *sd = sp + 64 * kPitch;
-  const bool keys = blockIdx.x < pieces;
-  const int piece = keys ? blockIdx.x : blockIdx.x - pieces;
+                                                             const __grid_constant__ AttendGradArgs a, int tiles) {
+  extern __shared__ __align__(16) float sm[];
+  constexpr int RI = R / 16;
+  float *r1 = sm, *r2 = r1 + R * (D + 4), *c1 = r2 + R * (D + 4), *c2 = c1 + 64 * (D + 4), *sp = c2 + 64 * (D + 4),
+        *sd = sp + R * kPitch;
+  const bool keys = blockIdx.x < tiles;
+  const int tile = keys ? blockIdx.x : blockIdx.x - tiles;
   const int h = blockIdx.y, b = blockIdx.z, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int N = a.N_valid, shift = a.block == 128 ? 1 : 0, W = (a.nB + 31) >> 5;
   const long long bh = static_cast<long long>(b) * a.H + h;
@@ -205,13 +212,15 @@ __global__ void __launch_bounds__(256) attend_grad_f32_kernel(const float* __res
   const GradStride &s_c1 = a.st[keys ? kQ : kK], &s_c2 = a.st[keys ? kDout : kV];
   const float* g1 = (keys ? q : k) + offset(s_c1, b, h, 0);
   const float* g2 = (keys ? dout : v) + offset(s_c2, b, h, 0);
-  const int r0 = piece * 64, mine = piece >> shift;
+  const float* neg_lse2 = a.neg_lse2 + bh * a.Npad;
+  const float* neg_delta = a.neg_delta + bh * a.Npad;
+  const int r0 = tile * R, mine = r0 / a.block;
   const float scale = 1.0f / sqrtf(static_cast<float>(D)), scale2 = scale * kLog2e;
-  load_piece<D>(r1, (keys ? k : q) + offset(s_r1, b, h, 0), s_r1.n, r0, N);
-  load_piece<D>(r2, (keys ? v : dout) + offset(s_r2, b, h, 0), s_r2.n, r0, N);
-  float acc1[4][D / 16], acc2[4][D / 16];
+  load_rows<D>(r1, (keys ? k : q) + offset(s_r1, b, h, 0), s_r1.n, r0, R, N);
+  load_rows<D>(r2, (keys ? v : dout) + offset(s_r2, b, h, 0), s_r2.n, r0, R, N);
+  float acc1[RI][D / 16], acc2[RI][D / 16];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RI; ++i)
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) acc1[i][j] = acc2[i][j] = 0.f;
   const uint32_t* list = (keys ? a.bits_t : a.bits) + (bh * a.nB + mine) * W;
@@ -224,35 +233,34 @@ __global__ void __launch_bounds__(256) attend_grad_f32_kernel(const float* __res
         const int c0 = (other << shift) * 64 + s * 64;
         if (c0 >= N) break;
         __syncthreads();          // the last piece's sums are done with c1, c2, sp, sd
-        load_piece<D>(c1, g1, s_c1.n, c0, N);
-        load_piece<D>(c2, g2, s_c2.n, c0, N);
+        load_rows<D>(c1, g1, s_c1.n, c0, 64, N);
+        load_rows<D>(c2, g2, s_c2.n, c0, 64, N);
         __syncthreads();
-        float p[4][4], g[4][4];
-        dots<D>(p, r1, c1, ty, tx);
-        dots<D>(g, r2, c2, ty, tx);
+        float p[RI][4], g[RI][4];
+        dots<D, RI>(p, r1, c1, ty, tx);
+        dots<D, RI>(g, r2, c2, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RI; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int row = ty + 16 * i, col = tx + 16 * j;
-            const int qi = keys ? col : row, ki = keys ? row : col;              // within their pieces
-            const int qn = (keys ? c0 : r0) + qi, kn = (keys ? r0 : c0) + ki;
-            const bool on = kn < N && ((set >> qi) & 1ull);
-            const float pr = on ? exp2f(fmaf(p[i][j], scale2, a.neg_lse2[bh * a.Npad + qn])) : 0.f;
+            const int qn = keys ? c0 + col : r0 + row, kn = keys ? r0 + row : c0 + col;
+            const bool on = kn < N && ((set >> (qn & 63)) & 1ull);     // qn < Npad: the tables are padded
+            const float pr = on ? exp2f(fmaf(p[i][j], scale2, neg_lse2[qn])) : 0.f;
             sp[row * kPitch + col] = pr;
-            sd[row * kPitch + col] = on ? pr * (g[i][j] + a.neg_delta[bh * a.Npad + qn]) : 0.f;
+            sd[row * kPitch + col] = on ? pr * (g[i][j] + neg_delta[qn]) : 0.f;
           }
         __syncthreads();
-        weighted<D>(acc1, sd, c1, ty, tx);
-        if (keys) weighted<D>(acc2, sp, c2, ty, tx);
+        weighted<D, RI>(acc1, sd, c1, ty, tx);
+        if (keys) weighted<D, RI>(acc2, sp, c2, ty, tx);
       }
     }
   }
   if (keys) {
-    store_rows<D>(static_cast<float*>(a.dk) + offset(a.st[kDk], b, h, 0), a.st[kDk].n, r0, N, acc1, scale, ty, tx);
-    store_rows<D>(static_cast<float*>(a.dv) + offset(a.st[kDv], b, h, 0), a.st[kDv].n, r0, N, acc2, 1.f, ty, tx);
+    store_rows<D, RI>(static_cast<float*>(a.dk) + offset(a.st[kDk], b, h, 0), a.st[kDk].n, r0, N, acc1, scale, ty, tx);
+    store_rows<D, RI>(static_cast<float*>(a.dv) + offset(a.st[kDv], b, h, 0), a.st[kDv].n, r0, N, acc2, 1.f, ty, tx);
   } else {
-    store_rows<D>(static_cast<float*>(a.dq) + offset(a.st[kDq], b, h, 0), a.st[kDq].n, r0, N, acc1, scale, ty, tx);
+    store_rows<D, RI>(static_cast<float*>(a.dq) + offset(a.st[kDq], b, h, 0), a.st[kDq].n, r0, N, acc1, scale, ty, tx);
   }
 }
 
@@ -268,14 +276,22 @@ cudaError_t prep(const void* out, const void* dout, const float* lse, const Atte
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, int R>
 cudaError_t f32(const float* q, const float* k, const float* v, const float* dout, const AttendGradArgs& a, cudaStream_t s) {
-  constexpr int smem = (4 * 64 * (D + 4) + 2 * 64 * kPitch) * 4;
-  cudaError_t e = cudaFuncSetAttribute(attend_grad_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = f32_smem<D, R>();
+  cudaError_t e = cudaFuncSetAttribute(attend_grad_f32_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int pieces = (a.N_valid + 63) / 64;
-  attend_grad_f32_kernel<D><<<dim3(2 * pieces, a.H, a.B), 256, smem, s>>>(q, k, v, dout, a, pieces);
+  const int tiles = (a.N_valid + R - 1) / R;
+  attend_grad_f32_kernel<D, R><<<dim3(2 * tiles, a.H, a.B), 256, smem, s>>>(q, k, v, dout, a, tiles);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t f32_rows(const float* q, const float* k, const float* v, const float* dout, const AttendGradArgs& a,
+                     cudaStream_t s) {
+  const long long ctas = 2ll * a.B * a.H * ((a.N_valid + 63) / 64);      // with R = 64
+  if (ctas >= 148) return f32<D, 64>(q, k, v, dout, a, s);
+  return ctas >= 74 ? f32<D, 32>(q, k, v, dout, a, s) : f32<D, 16>(q, k, v, dout, a, s);
 }
 
 }  // namespace
@@ -314,7 +330,7 @@ cudaError_t launch_attend_grad_prep(const void* out, const void* dout, const flo
 
 cudaError_t launch_attend_grad_f32(const float* q, const float* k, const float* v, const float* dout,
                                    const AttendGradArgs& a, cudaStream_t s) {
-  return a.d == 128 ? f32<128>(q, k, v, dout, a, s) : f32<64>(q, k, v, dout, a, s);
+  return a.d == 128 ? f32_rows<128>(q, k, v, dout, a, s) : f32_rows<64>(q, k, v, dout, a, s);
 }
 
 }  // namespace lbsa
