@@ -2,8 +2,8 @@
 // accumulate).  The mathematics and the tables are attend_grad.cu's.
 //
 // Two kinds of CTA in one launch, each owning 128 rows and walking the union of
-// its two 64-row blocks' lists in steps of 128 columns (two 64-row pieces of
-// the other side, which need not be neighbours):
+// its two 64-row blocks' lists in steps of 128 columns (two 64-row pieces of the
+// other side, which need not be neighbours):
 //   keys      S^T = K Q^T, dP^T = V dO^T (rows are keys, columns queries), then
 //             dV += P^T dO and dK += dS^T Q: four products a step
 //   queries   S = Q K^T, dP = dO V^T, then dQ += dS K: three products a step
@@ -11,64 +11,78 @@
 // added across CTAs: no atomics, no fp32 dQ in memory (a read-modify-write of
 // 64 KB a step) and the same bits on every call.
 //
-// Warp roles (320 threads, one CTA an SM):
-//   warps 0-3, 4-7  thread t owns row t % 128 = TMEM lane; the first four warps
-//             take a step's first piece (columns 0-63), the others the second.
-//             P = 2^(S scale - lse), packed to bf16 over the S columns just
-//             read (keys); dS = P (dP - D), over the dP columns; at the end the
-//             rows' sums.
-//   warp 8    TMA producer: walks the two bit rows, loads the CTA's own tiles
-//             once, then the first operand's pieces through a 3-stage and the
-//             second's through a 2-stage ring, each refilled when its own last
-//             product is done (keys: with lse and D of the columns).
-//   warp 9    UMMA issuer.
-// TMEM columns: [0,128) S, [128,256) dP, [256,256+D) dK or dQ, [384,384+D) dV.
-// A query tile has no dV: its q and dout rows take those columns, so that all
-// three of its products read their A operand from TMEM.  With both operands in
-// shared memory a 128 x 128 x 16 product reads 8 KB in the 64 cycles that the
-// tensor core needs for it, the whole bandwidth, and took 90 to 100 cycles.
+// Warp roles (18 warps, one CTA an SM):
+//   softmax   four warpgroups; thread t of each owns row t = TMEM lane
+//             and 32 of the step's columns.  P = 2^(S scale - lse), packed to
+//             bf16 over the S columns just read (keys); dS = P (dP - D), over
+//             the dP columns; at the end the rows' sums.
+//   producer  TMA: walks the two bit rows, loads the CTA's own tiles once, then
+//             the first operand's pieces through a 3-stage and the second's
+//             through a 2-stage ring, each refilled when its own last product
+//             is done (keys: with lse and D of the columns).
+//   issuer    UMMAs.
+// TMEM columns: S, dP, dK or dQ, dV.  A query tile has no dV: its q and dout
+// rows take those columns, so that all three of its products read their A
+// operand from TMEM.  With both operands in shared memory a 128 x 128 x 16
+// product reads 8 KB in the 64 cycles that the tensor core needs for it, the
+// whole bandwidth, and took 90 to 100 cycles.
 #include "lbsa_device.cuh"
 
 namespace lbsa {
 namespace {
 
-constexpr int BM = 128;             // rows of a tile, columns of a step
-#ifndef LBSA_GRAD_GROUPS
-#define LBSA_GRAD_GROUPS 4
-#endif
-#ifndef LBSA_GRAD_POLY8
-#define LBSA_GRAD_POLY8 4
-#endif
-constexpr int kGroups = LBSA_GRAD_GROUPS;        // softmax warpgroups, kCols columns of a step each
-constexpr int kCols = BM / kGroups;
-constexpr int kPoly8 = LBSA_GRAD_POLY8;
-constexpr int kProducer = kGroups * 4, kIssuer = kProducer + 1;     // their warps
-constexpr int kThreads = (kIssuer + 1) * 32;
+constexpr int BM = 128;             // rows of a tile
+constexpr int kCols = 32;           // columns of a step that a softmax warpgroup takes
 constexpr int N1 = 3, N2 = 2;       // ring depths of the two operands
+// Of every 8 groups of four logits kPoly8 take two of their exponentials on the
+// FMA pipe (a cubic, relative error 7.5e-5, far below the rounding of P and dS
+// to bf16, 2^-9), which unloads the MUFU: with 4 (a quarter of them) 8,192
+// dense tokens of 8 heads of 64 took 0.59 ms, with none 0.61.
+constexpr int kPoly8 = 4;
+constexpr int BN = 128;             // columns of a step, two 64-row pieces
+constexpr int kGroups = BN / kCols; // softmax warpgroups
+constexpr int kProducer = kGroups * 4, kIssuer = kProducer + 1;      // their warps
+constexpr int kThreads = (kIssuer + 1) * 32;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kS = 0, kDP = 128, kAcc1 = 256, kAcc2 = 384;
-constexpr uint32_t kRows1 = 384, kRows2 = 448;      // queries: the tile's q and dout, two bf16 a column
 
-template <int D>
+template <int D, bool KEYS>
 struct Layout {
-  static constexpr int TILE = BM * D * 2;
+  // S buffers: where the sums leave room for a second (keys, d = 64), S of the
+  // step after next is issued as soon as P has been read, instead of one later
+  static constexpr int SB = KEYS && D == 64 ? 2 : 1;
+  // TMEM columns
+  static constexpr uint32_t S = 0, DP = SB * BN, ACC1 = DP + BN, ACC2 = ACC1 + D;
+  static constexpr uint32_t ROWS1 = ACC2, ROWS2 = ACC2 + D / 2;      // queries: the tile's q and dout, two bf16 a column
+  // shared memory
+  static constexpr int TILE = BM * D * 2;                    // also a step's rows of one operand
   static constexpr int OFF_R1 = 0, OFF_R2 = TILE;
   static constexpr int OFF_C1 = 2 * TILE, OFF_C2 = OFF_C1 + N1 * TILE;
-  static constexpr int OFF_COL = OFF_C2 + N2 * TILE;         // per stage: 128 lse, 128 D
-  static constexpr int OFF_BAR = OFF_COL + N2 * 2 * BM * 4;
-  static constexpr int OFF_MISC = OFF_BAR + 18 * 8;          // tmem, abort, count, pad, entries[4][2]
-  static constexpr int BYTES = OFF_MISC + 48;
+  static constexpr int OFF_COL = OFF_C2 + N2 * TILE;         // per stage: BN lse, BN D
+  static constexpr int OFF_BAR = OFF_COL + N2 * 2 * BN * 4;
+  static constexpr int OFF_SETS = OFF_BAR + 20 * 8;          // per step of four: token sets [half][piece]
+  static constexpr int OFF_MISC = OFF_SETS + 4 * 4 * 8;      // tmem, abort, count, pad, entries[4][2]
+  [[maybe_unused]] static constexpr int BYTES = OFF_MISC + 48;
 };
+static_assert(Layout<128, true>::BYTES <= 227 * 1024, "shared memory of a CTA");
+
+// What a step's columns are: the piece of each 64 | kWhole where all its rows
+// exist | the halves of the tile that keep it << 30.
+constexpr uint32_t kPiece = 0x0FFFFFFFu, kWhole = 1u << 29;
 
 // c_empty: a step's last product is done (first operand's stage, columns' lse
-// and D); c2_empty: the second operand's last product is done.
+// and D); c2_empty: the second operand's last product is done.  s_full has two
+// arrivals, the UMMAs' completion and the issuer's own, which passes on what it
+// has waited for: the step's entry and (with one S buffer) its columns' values,
+// for which the softmax warps then need no wait of their own.  With two S
+// buffers the issuer may not wait for those: they come when step j - 2 is over,
+// which takes a product that it issues later.
 struct Bars {
   uint64_t *r_full, *c1_full, *c2_full, *col_full, *c_empty, *c2_empty, *s_full, *dp_full, *drain, *s_done, *ds_full;
 };
-constexpr int kBars = 18, kWarpBars = 16;      // from kWarpBars on every softmax warp arrives
+constexpr int kBars = 20, kSFull = 13, kWarpBars = 17;      // from kWarpBars on every softmax warp arrives
 __device__ __forceinline__ Bars make_bars(uint8_t* base) {
   uint64_t* b = reinterpret_cast<uint64_t*>(base);
-  return Bars{b, b + 1, b + 4, b + 6, b + 8, b + 11, b + 13, b + 14, b + 15, b + 16, b + 17};
+  return Bars{b, b + 1, b + 4, b + 6, b + 8, b + 11, b + kSFull, b + 15, b + 16, b + kWarpBars, b + 19};
 }
 
 // Bulk copy of `bytes` (a multiple of 16) into shared memory, counted on `bar`.
@@ -87,9 +101,10 @@ struct Tile {
 // The walk over a tile's kept pieces: the set bits of its two bit rows.
 struct Walk {
   const uint32_t *r0, *r1;          // r1: NULL for 128-row blocks and a missing second block
-  int W, w, shift, sub;
+  int W, w, shift, sub, N;
   uint32_t a, b, rest;              // words and their union's bits still to come
-  __device__ __forceinline__ void init(const uint32_t* x, const uint32_t* y, int words, int sh) {
+  __device__ __forceinline__ void init(const uint32_t* x, const uint32_t* y, int words, int sh, int n) {
+    N = n;
     r0 = x;
     r1 = y;
     W = words;
@@ -98,10 +113,10 @@ struct Walk {
     sub = 0;
     rest = 0u;
   }
-  // the next piece (64-row index) | the halves of the tile that keep it << 30; 0xFFFFFFFF at the end
+  // the next piece's entry; 0 at the end (a piece that is walked is kept by a half)
   __device__ __forceinline__ uint32_t next() {
     while (rest == 0u) {
-      if (++w >= W) return 0xFFFFFFFFu;
+      if (++w >= W) return 0u;
       a = __ldg(r0 + w);
       b = r1 ? __ldg(r1 + w) : (shift ? a : 0u);
       rest = a | b;
@@ -115,7 +130,7 @@ struct Walk {
     } else {
       sub = 1;
     }
-    return piece | (halves << 30);
+    return piece | ((piece + 1) * 64 <= static_cast<uint32_t>(N) ? kWhole : 0u) | (halves << 30);
   }
 };
 
@@ -130,11 +145,11 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-template <int D, bool KEYS>
+template <int D, bool KEYS, bool MASKED>
 __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const CUtensorMap* r1, const CUtensorMap* r2,
                                         const CUtensorMap* c1, const CUtensorMap* c2, const AttendGradArgs& a,
                                         const Tile& t, Walk walk, uint32_t* entries, volatile int* abort_flag) {
-  using L = Layout<D>;
+  using L = Layout<D, KEYS>;
   auto load = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int half, int piece) {
     for (int c = 0; c < D / 64; ++c) tma_load_4d(dst + c * BM * 128 + half * 64 * 128, m, bar, c * 64, piece * 64, t.h, t.b);
   };
@@ -146,17 +161,29 @@ __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const C
       load(smem + L::OFF_R2, r2, bars.r_full, p, t.tile * 2 + p);
     }
   }
-  uint32_t e[2], ahead[2];          // pieces of this step, of the next one
+  uint32_t e[2], ahead[2];          // entries of this step, of the next one
   int done1 = 0, done2 = 0, done_col = 0;
-  // step j's first operand into the stage that step j - 3 had
+  // step j's first operand into the stage that step j - 3 had, its entries into the slots that step j - 4 had
   auto first = [&](int j, int stage) {
     ahead[0] = walk.next();
     ahead[1] = walk.next();
-    if (ahead[1] == 0xFFFFFFFFu) ahead[1] = ahead[0] & 0x3FFFFFFFu;       // an odd tail: the piece again, kept by nobody
+    if (ahead[1] == 0u) ahead[1] = ahead[0] & kPiece;       // an odd tail: the piece again, kept by nobody
     entries[(j & 3) * 2] = ahead[0];
     entries[(j & 3) * 2 + 1] = ahead[1];
+    if (MASKED) {
+      // per-token lists: the query tokens of each (half, piece) pair that keep its key block
+      uint64_t* sets = reinterpret_cast<uint64_t*>(smem + L::OFF_SETS) + (j & 3) * 4;
+      uint64_t v[4];
+      for (int i = 0; i < 4; ++i) {
+        const long long mine = t.tile * 2 + (i >> 1), piece = ahead[i & 1] & kPiece;
+        v[i] = (ahead[i & 1] >> (30 + (i >> 1))) & 1u
+                   ? __ldg(a.masks_t + (t.bh * a.nB + (KEYS ? mine : piece)) * a.nB + (KEYS ? piece : mine))
+                   : 0ull;
+      }
+      for (int i = 0; i < 4; ++i) sets[i] = v[i];
+    }
     mbar_arrive_expect_tx(bars.c1_full + stage, L::TILE);
-    for (int p = 0; p < 2; ++p) load(smem + L::OFF_C1 + stage * L::TILE, c1, bars.c1_full + stage, p, ahead[p] & 0x3FFFFFFFu);
+    for (int p = 0; p < 2; ++p) load(smem + L::OFF_C1 + stage * L::TILE, c1, bars.c1_full + stage, p, ahead[p] & kPiece);
     done1 = j + 1;
   };
   first(0, 0);
@@ -167,18 +194,18 @@ __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const C
     if (j >= N2 && !mbar_wait(bars.c2_empty + (j & 1), ((j >> 1) & 1) ^ 1, a.wait_limit, a.status, abort_flag)) break;
     uint64_t* f2 = bars.c2_full + (j & 1);
     mbar_arrive_expect_tx(f2, L::TILE);
-    for (int p = 0; p < 2; ++p) load(smem + L::OFF_C2 + (j & 1) * L::TILE, c2, f2, p, e[p] & 0x3FFFFFFFu);
+    for (int p = 0; p < 2; ++p) load(smem + L::OFF_C2 + (j & 1) * L::TILE, c2, f2, p, e[p] & kPiece);
     done2 = j + 1;
     // step j - 2 is over: its columns' values and the stage that step j + 1 takes are free
     if (j >= 2 && !mbar_wait(bars.c_empty + stage, (((j - 2) / N1) & 1), a.wait_limit, a.status, abort_flag)) break;
     if (KEYS) {
       uint64_t* fc = bars.col_full + (j & 1);
-      mbar_arrive_expect_tx(fc, 2 * BM * 4);
+      mbar_arrive_expect_tx(fc, 2 * BN * 4);
       for (int p = 0; p < 2; ++p) {
-        const int piece = e[p] & 0x3FFFFFFFu;
-        float* col = reinterpret_cast<float*>(smem + L::OFF_COL) + (j & 1) * 2 * BM + p * 64;
+        const int piece = e[p] & kPiece;
+        float* col = reinterpret_cast<float*>(smem + L::OFF_COL) + (j & 1) * 2 * BN + p * 64;
         bulk_load(col, a.neg_lse2 + t.bh * a.Npad + piece * 64, 256, fc);
-        bulk_load(col + BM, a.neg_delta + t.bh * a.Npad + piece * 64, 256, fc);
+        bulk_load(col + BN, a.neg_delta + t.bh * a.Npad + piece * 64, 256, fc);
       }
       done_col = j + 1;
     }
@@ -197,29 +224,28 @@ __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const C
   }
 }
 
-// d[128 x 128] = x y^T over d; x, y: descriptors of K-major rows in shared memory
+// d[128 x BN] = x y^T over d; x, y: descriptors of K-major rows in shared memory
 template <int D>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint64_t x, uint64_t y) {
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const uint64_t off = ((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4;
-    umma_ss(d, x + off, y + off, idesc_bf16_f32(BM, BM, 0), kk > 0 ? 1u : 0u);
-  }
+  for (int kk = 0; kk < D / 16; ++kk)
+    umma_ss(d, x + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4), y + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4),
+            idesc_bf16_f32(BM, BN, 0), kk > 0 ? 1u : 0u);
 }
 // the same with x's rows packed in TMEM
 template <int D>
 __device__ __forceinline__ void mma_rows_ts(uint32_t d, uint32_t x, uint64_t y) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk)
-    umma_ts(d, x + kk * 8, y + (((kk >> 2) * (BM * 128) + (kk & 3) * 32) >> 4), idesc_bf16_f32(BM, BM, 0), kk > 0 ? 1u : 0u);
+    umma_ts(d, x + kk * 8, y + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), idesc_bf16_f32(BM, BN, 0), kk > 0 ? 1u : 0u);
 }
-// d[128 x D] += p y; p packed in TMEM (each warpgroup's kCols columns start `pitch` further), y: MN-major rows
+// d[128 x D] += p y; p packed in TMEM (each warpgroup's columns start kCols further), y: MN-major rows
 template <int D>
-__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t p, uint32_t pitch, uint64_t y, bool first) {
+__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t p, uint64_t y, bool first) {
   constexpr int PER = kCols / 16;
 #pragma unroll
-  for (int kk = 0; kk < BM / 16; ++kk)
-    umma_ts(d, p + (kk / PER) * pitch + (kk % PER) * 8, y + kk * (2048 >> 4), idesc_bf16_f32(BM, D, 1),
+  for (int kk = 0; kk < BN / 16; ++kk)
+    umma_ts(d, p + (kk / PER) * kCols + (kk % PER) * 8, y + kk * (2048 >> 4), idesc_bf16_f32(BM, D, 1),
             (!first || kk > 0) ? 1u : 0u);
 }
 
@@ -227,36 +253,41 @@ __device__ __forceinline__ void mma_sum(uint32_t d, uint32_t p, uint32_t pitch, 
 // warp-uniform, and one elected lane issues: with a single lane in the loop the
 // operands went through per-thread registers and an instruction took about 100
 // cycles to issue, where the tensor core needs 64 for it.
-// c_empty is a ring of three: the producer loads step j's second operand before
-// it waits for the end of step j - 2, so that on a pair step j's end could come
-// first and the phase be missed.  Every other barrier's next phase needs an
-// instruction that follows the wait for the last one.
+// Rings are as long as a barrier's phase could be missed otherwise.  c_empty is
+// three: the producer loads step j's second operand before it waits for the end
+// of step j - 2, so that on a pair step j's end could come first.  With two S
+// buffers S of step j + 1 is issued before P of step j is waited for: s_full and
+// s_done are pairs.  Every other barrier's next phase needs an instruction that
+// follows the wait for the last one.
 // tcgen05.mma instructions of one thread complete in the order of their issue:
 // S of step j + 1 may follow the product that reads P of step j from the same
 // columns, and dP the one that reads dS.
 template <int D, bool KEYS>
 __device__ __forceinline__ void issue(uint8_t* smem, const Bars& bars, uint32_t tmem, const AttendGradArgs& a,
                                       int n_steps, volatile int* abort_flag) {
-  using L = Layout<D>;
+  using L = Layout<D, KEYS>;
   const uint64_t r1 = smem_desc_sw128(smem_u32(smem + L::OFF_R1), 16, 1024), r2 = r1 + ((L::OFF_R2 - L::OFF_R1) >> 4);
   const uint64_t c1 = r1 + ((L::OFF_C1 - L::OFF_R1) >> 4), c2 = r1 + ((L::OFF_C2 - L::OFF_R1) >> 4);
-  const uint64_t m1 = smem_desc_sw128(smem_u32(smem + L::OFF_C1), BM * 128, 1024), m2 = m1 + ((L::OFF_C2 - L::OFF_C1) >> 4);
+  const uint64_t m1 = smem_desc_sw128(smem_u32(smem + L::OFF_C1), BN * 128, 1024), m2 = m1 + ((L::OFF_C2 - L::OFF_C1) >> 4);
   constexpr uint64_t STAGE = L::TILE >> 4;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool ok = warp_wait(bar, parity, a.wait_limit, a.status, abort_flag);
     tc_fence_after();
     return ok;
   };
-  int st = 0, st_next = 0, ph_next = 0;         // first operand's ring: this step's stage; the next S's stage and phase
-  auto s_of = [&](int) {
+  int st_next = 0, ph_next = 0;                 // the first operand's ring: stage and phase of the next S
+  auto s_of = [&](int j) {
+    const int buf = j & (L::SB - 1);
     if (!wait(bars.c1_full + st_next, ph_next)) return false;
     if (elect_one()) {
-      if (KEYS) mma_rows<D>(tmem + kS, r1, c1 + st_next * STAGE);
-      else mma_rows_ts<D>(tmem + kS, tmem + kRows1, c1 + st_next * STAGE);
-      umma_commit(bars.s_full);
+      if (KEYS) mma_rows<D>(tmem + L::S + buf * BN, r1, c1 + st_next * STAGE);
+      else mma_rows_ts<D>(tmem + L::S, tmem + L::ROWS1, c1 + st_next * STAGE);
+      umma_commit(bars.s_full + buf);
     }
     __syncwarp();
-    st = st_next;
+    if (KEYS && L::SB == 1 && !wait(bars.col_full + (j & 1), (j >> 1) & 1)) return false;
+    if (elect_one()) mbar_arrive(bars.s_full + buf);
+    __syncwarp();
     if (++st_next == N1) {
       st_next = 0;
       ph_next ^= 1;
@@ -266,34 +297,35 @@ __device__ __forceinline__ void issue(uint8_t* smem, const Bars& bars, uint32_t 
   auto dp_of = [&](int j) {
     if (!wait(bars.c2_full + (j & 1), (j >> 1) & 1)) return false;
     if (elect_one()) {
-      if (KEYS) mma_rows<D>(tmem + kDP, r2, c2 + (j & 1) * STAGE);
-      else mma_rows_ts<D>(tmem + kDP, tmem + kRows2, c2 + (j & 1) * STAGE);
+      if (KEYS) mma_rows<D>(tmem + L::DP, r2, c2 + (j & 1) * STAGE);
+      else mma_rows_ts<D>(tmem + L::DP, tmem + L::ROWS2, c2 + (j & 1) * STAGE);
       umma_commit(bars.dp_full);
       if (!KEYS) umma_commit(bars.c2_empty + (j & 1));
     }
     __syncwarp();
     return true;
   };
-  bool ok = n_steps > 0 && wait(bars.r_full, 0) && s_of(0) && dp_of(0);
+  bool ok = n_steps > 0 && wait(bars.r_full, 0) && s_of(0) && dp_of(0) && (L::SB == 1 || n_steps == 1 || s_of(1));
+  int st = 0;                                   // step j's stage of the first operand
   for (int j = 0; ok && j < n_steps; ++j) {
-    const bool more = j + 1 < n_steps;
-    const int mine = st;                        // step j's stage of the first operand
-    if (!wait(bars.s_done, j & 1)) break;
+    const int buf = j & (L::SB - 1);
+    if (!wait(bars.s_done + buf, (j / L::SB) & 1)) break;
     if (KEYS) {
       if (elect_one()) {
-        mma_sum<D>(tmem + kAcc2, tmem + kS, kCols, m2 + (j & 1) * STAGE, j == 0);
+        mma_sum<D>(tmem + L::ACC2, tmem + L::S + buf * BN, m2 + (j & 1) * STAGE, j == 0);
         umma_commit(bars.c2_empty + (j & 1));
       }
       __syncwarp();
     }
-    if (more && !s_of(j + 1)) break;
+    if (j + L::SB < n_steps && !s_of(j + L::SB)) break;
     if (!wait(bars.ds_full, j & 1)) break;
     if (elect_one()) {
-      mma_sum<D>(tmem + kAcc1, tmem + kDP, kCols, m1 + mine * STAGE, j == 0);
-      umma_commit(bars.c_empty + mine);
+      mma_sum<D>(tmem + L::ACC1, tmem + L::DP, m1 + st * STAGE, j == 0);
+      umma_commit(bars.c_empty + st);
     }
     __syncwarp();
-    if (more && !dp_of(j + 1)) break;
+    if (++st == N1) st = 0;
+    if (j + 1 < n_steps && !dp_of(j + 1)) break;
   }
   // every UMMA has completed before the sums are read and TMEM is released
   if (elect_one()) umma_commit(bars.drain);
@@ -301,13 +333,13 @@ __device__ __forceinline__ void issue(uint8_t* smem, const Bars& bars, uint32_t 
   mbar_wait(bars.drain, 0, a.wait_limit, a.status, nullptr);
 }
 
-// P of CPT columns in place of their logits (r), then dS = P (dP - D) in place
+// P of a thread's columns in place of their logits (r), then dS = P (dP - D) in place
 // of dP.  neg_lse / neg_delta: of the columns (keys) or of the row (queries).
-template <int CPT, bool KEYS>
-__device__ __forceinline__ void probabilities(uint32_t (&r)[CPT], const float* neg_lse, float row_neg_lse, float scale_log2) {
+template <bool KEYS>
+__device__ __forceinline__ void probabilities(uint32_t (&r)[kCols], const float* neg_lse, float row_neg_lse, float scale_log2) {
   const unsigned long long sc2 = f2_as_u64(scale_log2, scale_log2);
 #pragma unroll
-  for (int c = 0; c < CPT; c += 4) {
+  for (int c = 0; c < kCols; c += 4) {
     ulonglong2 l = make_ulonglong2(f2_as_u64(row_neg_lse, row_neg_lse), f2_as_u64(row_neg_lse, row_neg_lse));
     if (KEYS) l = *reinterpret_cast<const ulonglong2*>(neg_lse + c);
     float v[4];
@@ -317,11 +349,11 @@ __device__ __forceinline__ void probabilities(uint32_t (&r)[CPT], const float* n
     for (int i = 0; i < 4; ++i) r[c + i] = __float_as_uint((c / 4 * kPoly8) % 8 < kPoly8 && i < 2 ? exp2_poly3(v[i]) : ex2(v[i]));
   }
 }
-template <int CPT, bool KEYS>
-__device__ __forceinline__ void score_gradients(uint32_t (&g)[CPT], const uint32_t (&p)[CPT], const float* neg_delta,
+template <bool KEYS>
+__device__ __forceinline__ void score_gradients(uint32_t (&g)[kCols], const uint32_t (&p)[kCols], const float* neg_delta,
                                                 float row_neg_delta) {
 #pragma unroll
-  for (int c = 0; c < CPT; c += 4) {
+  for (int c = 0; c < kCols; c += 4) {
     ulonglong2 d = make_ulonglong2(f2_as_u64(row_neg_delta, row_neg_delta), f2_as_u64(row_neg_delta, row_neg_delta));
     if (KEYS) d = *reinterpret_cast<const ulonglong2*>(neg_delta + c);
 #pragma unroll
@@ -335,21 +367,12 @@ __device__ __forceinline__ void score_gradients(uint32_t (&g)[CPT], const uint32
   }
 }
 
-template <int CPT>
-__device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&r)[CPT]) {
-#pragma unroll
-  for (int c = 0; c < CPT; c += 32) tmem_ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&r[c]));
-  tmem_wait_ld_dep(*reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-  if (CPT == 64) reg_dep(*reinterpret_cast<uint32_t(*)[32]>(&r[CPT - 32]));
-}
 // rounded to bf16, two a column
-template <int CPT>
-__device__ __forceinline__ void store_packed(uint32_t taddr, const uint32_t (&r)[CPT]) {
-  uint32_t pk[CPT / 2];
+__device__ __forceinline__ void store_packed(uint32_t taddr, const uint32_t (&r)[kCols]) {
+  uint32_t pk[kCols / 2];
 #pragma unroll
-  for (int c = 0; c < CPT / 2; ++c) pk[c] = pack_bf16x2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
-  if constexpr (CPT == 64) tmem_st32(taddr, pk);
-  else tmem_st16(taddr, pk);
+  for (int c = 0; c < kCols / 2; ++c) pk[c] = pack_bf16x2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
+  tmem_st16(taddr, pk);
   tmem_wait_st();
 }
 
@@ -357,24 +380,23 @@ template <int D, bool KEYS, bool MASKED>
 __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_t tmem, const AttendGradArgs& a,
                                         const Tile& t, const uint32_t* entries, float scale_log2, float scale,
                                         volatile int* abort_flag) {
-  using L = Layout<D>;
-  constexpr int CPT = kCols;
+  using L = Layout<D, KEYS>;
   const int lane = threadIdx.x & 31, wg = threadIdx.x >> 7, row = threadIdx.x & 127;
   const int half = row >> 6, grow = t.tile * BM + row;
-  const int c0 = wg * CPT, p = c0 >> 6, in_piece = c0 & 63;          // the thread's columns, their piece of the step
+  const int c0 = wg * kCols, p = c0 >> 6, in_piece = c0 & 63;          // the thread's columns, their piece of the step
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(row & ~31) << 16);
-  const uint32_t s_col = t_lane + kS + c0, dp_col = t_lane + kDP + c0;
+  const uint32_t s_col = t_lane + L::S + c0, dp_col = t_lane + L::DP + c0;
   const long long wl = a.wait_limit;
   float neg_lse = 0.f, neg_delta = 0.f;
   if (!KEYS && t.n_steps > 0) {
     neg_lse = a.neg_lse2[t.bh * a.Npad + grow];
     neg_delta = a.neg_delta[t.bh * a.Npad + grow];
     // the tile's own rows into TMEM: each warpgroup a part of q's or dout's row
-    constexpr int PART = 4 / kGroups * D / 4;      // 32-bit words
+    constexpr int PART = D / kGroups;              // 32-bit words: D / 2 a row, two warpgroups a tensor
     const GradStride& st = a.st[wg & 1 ? kDout : kQ];
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(wg & 1 ? a.dout : a.q) + t.b * st.b +
                                                       t.h * st.h + grow * st.n) + (wg >> 1) * (PART / 4);
-    const uint32_t dst = t_lane + (wg & 1 ? kRows2 : kRows1) + (wg >> 1) * PART;
+    const uint32_t dst = t_lane + (wg & 1 ? L::ROWS2 : L::ROWS1) + (wg >> 1) * PART;
 #pragma unroll
     for (int c = 0; c < PART; c += 16) {
       uint32_t v[16];
@@ -391,61 +413,57 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
     tmem_wait_st();
     warp_arrive(bars.r_full, lane);
   }
+  const uint64_t* sets = reinterpret_cast<const uint64_t*>(smem + L::OFF_SETS);
   bool alive = true;
-  int stage = 0, phase = 0;         // of the first operand's ring
   for (int j = 0; j < t.n_steps; ++j) {
-    alive = warp_wait(bars.c1_full + stage, phase, wl, a.status, abort_flag);
-    if (!alive) break;
-    if (++stage == N1) {
-      stage = 0;
-      phase ^= 1;
-    }
-    const uint32_t e = entries[(j & 3) * 2 + p];
-    const int piece = e & 0x3FFFFFFFu;
-    const bool take = (e >> (30 + half)) & 1u;                       // the same for the warp
-    // the thread's columns that count, as bits from bit 0
-    uint64_t on = ~0ull;
-    if (MASKED && take) {
-      if (KEYS) on = __ldg(a.masks_t + (t.bh * a.nB + t.tile * 2 + half) * a.nB + piece) >> in_piece;
-      else on = ((__ldg(a.masks_t + (t.bh * a.nB + piece) * a.nB + t.tile * 2 + half) >> (row & 63)) & 1ull) ? ~0ull : 0ull;
-    }
-    if (!KEYS) {
-      const int valid = a.N_valid - piece * 64 - in_piece;
-      if (valid < CPT) on &= valid > 0 ? (1ull << valid) - 1ull : 0ull;
-    }
-    if (!take) on = 0ull;
-    const bool all = !MASKED && take && (KEYS || a.N_valid - piece * 64 - in_piece >= CPT);   // the same for the warp
-    const float* col = reinterpret_cast<const float*>(smem + L::OFF_COL) + (j & 1) * 2 * BM + c0;
-    if (KEYS) {
+    const int buf = j & (L::SB - 1);
+    if (KEYS && L::SB == 2) {
       alive = warp_wait(bars.col_full + (j & 1), (j >> 1) & 1, wl, a.status, abort_flag);
       if (!alive) break;
     }
-    alive = warp_wait(bars.s_full, j & 1, wl, a.status, abort_flag);
+    alive = warp_wait(bars.s_full + buf, (j / L::SB) & 1, wl, a.status, abort_flag);
     if (!alive) break;
     tc_fence_after();
-    uint32_t r[CPT], g[CPT];
-    load_cols<CPT>(s_col, r);
+    uint32_t r[kCols], g[kCols];
+    tmem_ld32(s_col + buf * BN, r);
+    const float* col = reinterpret_cast<const float*>(smem + L::OFF_COL) + (j & 1) * 2 * BN + c0;
+    const uint32_t e = entries[(j & 3) * 2 + p];
+    // every column counts (the same for the warp); otherwise those of `on`, from bit 0
+    const bool all = !MASKED && ((e >> (30 + half)) & 1u) && (KEYS || (e & kWhole));
+    uint32_t on = 0u;
+    if (!all) {
+      const int valid = a.N_valid - static_cast<int>(e & kPiece) * 64 - in_piece;
+      if (MASKED) {
+        const uint64_t set = sets[(j & 3) * 4 + half * 2 + p];
+        on = KEYS ? static_cast<uint32_t>(set >> in_piece) : ((set >> (row & 63)) & 1ull) ? 0xFFFFFFFFu : 0u;
+      } else if ((e >> (30 + half)) & 1u) {
+        on = 0xFFFFFFFFu;
+      }
+      if (!KEYS && valid < kCols) on &= valid > 0 ? (1u << valid) - 1u : 0u;
+    }
+    tmem_wait_ld_dep(r);
     if (!KEYS) warp_arrive(bars.s_done, lane);                       // the S columns are free
-    probabilities<CPT, KEYS>(r, col, neg_lse, scale_log2);
+    probabilities<KEYS>(r, col, neg_lse, scale_log2);
     if (!all) {
 #pragma unroll
-      for (int c = 0; c < CPT; ++c) r[c] = ((on >> c) & 1ull) ? r[c] : 0u;
+      for (int c = 0; c < kCols; ++c) r[c] = ((on >> c) & 1u) ? r[c] : 0u;
     }
     if (KEYS) {
-      store_packed<CPT>(s_col, r);
-      warp_arrive(bars.s_done, lane);
+      store_packed(s_col + buf * BN, r);
+      warp_arrive(bars.s_done + buf, lane);
     }
     alive = warp_wait(bars.dp_full, j & 1, wl, a.status, abort_flag);
     if (!alive) break;
     tc_fence_after();
-    load_cols<CPT>(dp_col, g);
-    score_gradients<CPT, KEYS>(g, r, col + BM, neg_delta);
+    tmem_ld32(dp_col, g);
+    tmem_wait_ld_dep(g);
+    score_gradients<KEYS>(g, r, col + BN, neg_delta);
     if (!all) {
       // a pair that is not kept gets 0, whatever its dP holds
 #pragma unroll
-      for (int c = 0; c < CPT; ++c) g[c] = ((on >> c) & 1ull) ? g[c] : 0u;
+      for (int c = 0; c < kCols; ++c) g[c] = ((on >> c) & 1u) ? g[c] : 0u;
     }
-    store_packed<CPT>(dp_col, g);
+    store_packed(dp_col, g);
     warp_arrive(bars.ds_full, lane);
   }
   // ---- the rows' sums
@@ -477,10 +495,10 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
     }
   };
   if (KEYS) {
-    store(kAcc1, a.dk, a.st[kDk], scale);
-    store(kAcc2, a.dv, a.st[kDv], 1.f);
+    store(L::ACC1, a.dk, a.st[kDk], scale);
+    store(L::ACC2, a.dv, a.st[kDv], 1.f);
   } else {
-    store(kAcc1, a.dq, a.st[kDq], scale);
+    store(L::ACC1, a.dq, a.st[kDq], scale);
   }
 }
 
@@ -488,7 +506,7 @@ template <int D, bool KEYS, bool MASKED>
 __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, const CUtensorMap* tk,
                                          const CUtensorMap* tv, const CUtensorMap* tdo, const AttendGradArgs& a, int tile,
                                          float scale_log2, float scale) {
-  using L = Layout<D>;
+  using L = Layout<D, KEYS>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Bars bars = make_bars(smem + L::OFF_BAR);
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
@@ -496,7 +514,7 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
   uint32_t* entries = misc + 4;
   if (threadIdx.x == 0) {
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-    for (int i = 0; i < kBars; ++i) mbar_init(b + i, i >= kWarpBars || (i == 0 && !KEYS) ? kGroups * 4 : 1);   // r_full is barrier 0
+    for (int i = 0; i < kBars; ++i) mbar_init(b + i, i >= kWarpBars || (i == 0 && !KEYS) ? kGroups * 4 : (i == kSFull || i == kSFull + 1) ? 2 : 1);   // 0: r_full
     misc[1] = 0;
     misc[2] = 0;
     fence_barrier_init();
@@ -531,9 +549,9 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
   if (warp == kProducer) {
     if (lane == 0) {
       Walk walk;
-      walk.init(row0, row1, W, shift);
-      if (KEYS) produce<D, KEYS>(smem, bars, tk, tv, tq, tdo, a, t, walk, entries, abort_flag);
-      else produce<D, KEYS>(smem, bars, tq, tdo, tk, tv, a, t, walk, entries, abort_flag);
+      walk.init(row0, row1, W, shift, a.N_valid);
+      if (KEYS) produce<D, KEYS, MASKED>(smem, bars, tk, tv, tq, tdo, a, t, walk, entries, abort_flag);
+      else produce<D, KEYS, MASKED>(smem, bars, tq, tdo, tk, tv, a, t, walk, entries, abort_flag);
     }
   } else if (warp == kIssuer) {
     issue<D, KEYS>(smem, bars, tmem, a, t.n_steps, abort_flag);
@@ -575,10 +593,10 @@ cudaError_t launch_attend_grad_tc(const CUtensorMap* tq, const CUtensorMap* tk, 
     return cudaGetLastError();
   };
   if (a.d == 128)
-    return a.masks ? go(attend_grad_tc_kernel<128, true>, Layout<128>::BYTES)
-                   : go(attend_grad_tc_kernel<128, false>, Layout<128>::BYTES);
-  return a.masks ? go(attend_grad_tc_kernel<64, true>, Layout<64>::BYTES)
-                 : go(attend_grad_tc_kernel<64, false>, Layout<64>::BYTES);
+    return a.masks ? go(attend_grad_tc_kernel<128, true>, Layout<128, true>::BYTES)
+                   : go(attend_grad_tc_kernel<128, false>, Layout<128, true>::BYTES);
+  return a.masks ? go(attend_grad_tc_kernel<64, true>, Layout<64, true>::BYTES)
+                 : go(attend_grad_tc_kernel<64, false>, Layout<64, true>::BYTES);
 }
 
 }  // namespace lbsa
