@@ -29,24 +29,36 @@ __device__ __forceinline__ long long offset(const GradStride& s, int b, int h, i
   return b * s.b + h * s.h + n * s.n;
 }
 
-template <typename T>
-__device__ __forceinline__ float2 load2(const T* p);
-template <>
-__device__ __forceinline__ float2 load2<float>(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
-template <>
-__device__ __forceinline__ float2 load2<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+// sum of the products of 16 bytes of two rows
+__device__ __forceinline__ float dot16(uint4 x, uint4 y, float) {
+  float s = __uint_as_float(x.x) * __uint_as_float(y.x);
+  s = fmaf(__uint_as_float(x.y), __uint_as_float(y.y), s);
+  s = fmaf(__uint_as_float(x.z), __uint_as_float(y.z), s);
+  return fmaf(__uint_as_float(x.w), __uint_as_float(y.w), s);
 }
+__device__ __forceinline__ float dot16(uint4 x, uint4 y, __nv_bfloat16) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), s);
+    s = fmaf(__uint_as_float(a[i] & 0xFFFF0000u), __uint_as_float(b[i] & 0xFFFF0000u), s);
+  }
+  return s;
+}
+
+constexpr int kRowsPerBlock = 64;        // query rows of a block of the second kind; divides 128
 
 // Blocks [0, index_blocks): 32 query blocks of one (batch, head) each, whose
 // lists become bit rows and, transposed in shared memory, one word of every
-// key block's bits.  The others: one warp a query row, D = dout . out.
+// key block's bits.  The others: 64 query rows each, D = dout . out.  Bound by
+// reading out and dout once.
 template <typename T, int D>
 __global__ void __launch_bounds__(kPrepThreads)
 attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, const float* __restrict__ lse,
                         AttendGradArgs a, int index_blocks) {
   extern __shared__ uint32_t bm[];                     // [32][W]
+  grid_launch_dependents();
   const int W = (a.nB + 31) >> 5;
   if (blockIdx.x < index_blocks) {
     const int w = blockIdx.x % W;
@@ -82,29 +94,30 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
     }
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x - index_blocks) * (kPrepThreads / 32) + (threadIdx.x >> 5);
-  const long long bh = row / a.Npad;
-  const int n = static_cast<int>(row - bh * a.Npad);
-  if (bh >= static_cast<long long>(a.B) * a.H) return;
-  float sum = 0.f, l = -INFINITY;
-  if (n < a.N_valid) {
-    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<long long>(b) * a.H);
-    const T* po = out + offset(a.st[kOut], b, h, n) + lane * 2;
-    const T* pd = dout + offset(a.st[kDout], b, h, n) + lane * 2;
+  // a row is held by LANES lanes, 16 bytes each
+  constexpr int LANES = D * sizeof(T) / 16, GROUPS = kPrepThreads / LANES;
+  const int lane = threadIdx.x % LANES;
+  const long long row0 = static_cast<long long>(blockIdx.x - index_blocks) * kRowsPerBlock;   // of one (batch, head)
+  const long long bh = row0 / a.Npad;
+  const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<long long>(b) * a.H);
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) {
-      const float2 x = load2<T>(po + e * 64), y = load2<T>(pd + e * 64);
-      sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
+  for (int i = 0; i < kRowsPerBlock / GROUPS; ++i) {
+    const long long row = row0 + i * GROUPS + threadIdx.x / LANES;
+    const int n = static_cast<int>(row - bh * a.Npad);
+    float sum = 0.f, l = -INFINITY;
+    if (n < a.N_valid) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(out + offset(a.st[kOut], b, h, n)) + lane);
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(dout + offset(a.st[kDout], b, h, n)) + lane);
+      sum = dot16(x, y, T());
+      l = __ldg(lse + bh * a.N_valid + n);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    l = __ldg(lse + bh * a.N_valid + n);
-  }
-  if (lane == 0) {
-    const bool none = l == -INFINITY;
-    a.neg_lse2[row] = none ? -INFINITY : -l * kLog2e;
-    a.neg_delta[row] = none ? 0.f : -sum;
+    for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      const bool none = l == -INFINITY;
+      a.neg_lse2[row] = none ? -INFINITY : -l * kLog2e;
+      a.neg_delta[row] = none ? 0.f : -sum;
+    }
   }
 }
 
@@ -223,9 +236,10 @@ __global__ void __launch_bounds__(256) attend_grad_f32_kernel(const float* __res
   for (int i = 0; i < RI; ++i)
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) acc1[i][j] = acc2[i][j] = 0.f;
+  grid_wait();
   const uint32_t* list = (keys ? a.bits_t : a.bits) + (bh * a.nB + mine) * W;
   for (int w = 0; w < W; ++w) {
-    for (uint32_t word = __ldg(list + w); word; word &= word - 1) {
+    for (uint32_t word = list[w]; word; word &= word - 1) {
       const int other = w * 32 + __ffs(word) - 1;
       uint64_t set = ~0ull;       // per-token lists: the query tokens that keep the key block
       if (a.masks) set = a.masks_t[(bh * a.nB + (keys ? mine : other)) * a.nB + (keys ? other : mine)];
@@ -269,7 +283,7 @@ size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 template <typename T, int D>
 cudaError_t prep(const void* out, const void* dout, const float* lse, const AttendGradArgs& a, cudaStream_t s) {
   const long long W = (a.nB + 31) / 32, bh = static_cast<long long>(a.B) * a.H;
-  const long long index_blocks = bh * W, row_blocks = bh * a.Npad / (kPrepThreads / 32);
+  const long long index_blocks = bh * W, row_blocks = bh * a.Npad / kRowsPerBlock;
   if (index_blocks + row_blocks > 2147483647ll) return cudaErrorInvalidValue;
   attend_grad_prep_kernel<T, D><<<static_cast<unsigned>(index_blocks + row_blocks), kPrepThreads, 32 * W * 4, s>>>(
       static_cast<const T*>(out), static_cast<const T*>(dout), lse, a, static_cast<int>(index_blocks));
@@ -282,8 +296,8 @@ cudaError_t f32(const float* q, const float* k, const float* v, const float* dou
   cudaError_t e = cudaFuncSetAttribute(attend_grad_f32_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int tiles = (a.N_valid + R - 1) / R;
-  attend_grad_f32_kernel<D, R><<<dim3(2 * tiles, a.H, a.B), 256, smem, s>>>(q, k, v, dout, a, tiles);
-  return cudaGetLastError();
+  return launch_dependent(attend_grad_f32_kernel<D, R>, dim3(2 * tiles, a.H, a.B), dim3(256), smem, s, q, k, v, dout, a,
+                          tiles);
 }
 
 template <int D>

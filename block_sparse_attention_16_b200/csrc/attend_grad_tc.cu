@@ -61,9 +61,10 @@ struct Layout {
   static constexpr int OFF_BAR = OFF_COL + N2 * 2 * BN * 4;
   static constexpr int OFF_SETS = OFF_BAR + 20 * 8;          // per step of four: token sets [half][piece]
   static constexpr int OFF_MISC = OFF_SETS + 4 * 4 * 8;      // tmem, abort, count, pad, entries[4][2]
-  [[maybe_unused]] static constexpr int BYTES = OFF_MISC + 48;
 };
-static_assert(Layout<128, true>::BYTES <= 227 * 1024, "shared memory of a CTA");
+template <int D>
+constexpr int kSmemBytes = Layout<D, true>::OFF_MISC + 48;
+static_assert(kSmemBytes<128> <= 227 * 1024, "shared memory of a CTA");
 
 // What a step's columns are: the piece of each 64 | kWhole where all its rows
 // exist | the halves of the tile that keep it << 30.
@@ -117,8 +118,8 @@ struct Walk {
   __device__ __forceinline__ uint32_t next() {
     while (rest == 0u) {
       if (++w >= W) return 0u;
-      a = __ldg(r0 + w);
-      b = r1 ? __ldg(r1 + w) : (shift ? a : 0u);
+      a = r0[w];
+      b = r1 ? r1[w] : (shift ? a : 0u);
       rest = a | b;
     }
     const int bit = __ffs(rest) - 1;
@@ -145,21 +146,20 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
+// 64 rows into the `half` of a 128-row buffer
+template <int D>
+__device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int half, int piece, const Tile& t) {
+  for (int c = 0; c < D / 64; ++c) tma_load_4d(dst + c * BM * 128 + half * 64 * 128, m, bar, c * 64, piece * 64, t.h, t.b);
+}
+
 template <int D, bool KEYS, bool MASKED>
-__device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const CUtensorMap* r1, const CUtensorMap* r2,
-                                        const CUtensorMap* c1, const CUtensorMap* c2, const AttendGradArgs& a,
-                                        const Tile& t, Walk walk, uint32_t* entries, volatile int* abort_flag) {
+__device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const CUtensorMap* c1, const CUtensorMap* c2,
+                                        const AttendGradArgs& a, const Tile& t, Walk walk, uint32_t* entries,
+                                        volatile int* abort_flag) {
   using L = Layout<D, KEYS>;
-  auto load = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int half, int piece) {
-    for (int c = 0; c < D / 64; ++c) tma_load_4d(dst + c * BM * 128 + half * 64 * 128, m, bar, c * 64, piece * 64, t.h, t.b);
-  };
-  if (t.n_steps == 0) return;
-  if (KEYS) {
-    mbar_arrive_expect_tx(bars.r_full, 2 * L::TILE);
-    for (int p = 0; p < 2; ++p) {
-      load(smem + L::OFF_R1, r1, bars.r_full, p, t.tile * 2 + p);
-      load(smem + L::OFF_R2, r2, bars.r_full, p, t.tile * 2 + p);
-    }
+  if (t.n_steps == 0) {
+    if (KEYS) mbar_wait(bars.r_full, 0, a.wait_limit, a.status, nullptr);      // the own rows land before the CTA exits
+    return;
   }
   uint32_t e[2], ahead[2];          // entries of this step, of the next one
   int done1 = 0, done2 = 0, done_col = 0;
@@ -177,13 +177,13 @@ __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const C
       for (int i = 0; i < 4; ++i) {
         const long long mine = t.tile * 2 + (i >> 1), piece = ahead[i & 1] & kPiece;
         v[i] = (ahead[i & 1] >> (30 + (i >> 1))) & 1u
-                   ? __ldg(a.masks_t + (t.bh * a.nB + (KEYS ? mine : piece)) * a.nB + (KEYS ? piece : mine))
+                   ? a.masks_t[(t.bh * a.nB + (KEYS ? mine : piece)) * a.nB + (KEYS ? piece : mine)]
                    : 0ull;
       }
       for (int i = 0; i < 4; ++i) sets[i] = v[i];
     }
     mbar_arrive_expect_tx(bars.c1_full + stage, L::TILE);
-    for (int p = 0; p < 2; ++p) load(smem + L::OFF_C1 + stage * L::TILE, c1, bars.c1_full + stage, p, ahead[p] & kPiece);
+    for (int p = 0; p < 2; ++p) load_rows<D>(smem + L::OFF_C1 + stage * L::TILE, c1, bars.c1_full + stage, p, ahead[p] & kPiece, t);
     done1 = j + 1;
   };
   first(0, 0);
@@ -194,7 +194,7 @@ __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const C
     if (j >= N2 && !mbar_wait(bars.c2_empty + (j & 1), ((j >> 1) & 1) ^ 1, a.wait_limit, a.status, abort_flag)) break;
     uint64_t* f2 = bars.c2_full + (j & 1);
     mbar_arrive_expect_tx(f2, L::TILE);
-    for (int p = 0; p < 2; ++p) load(smem + L::OFF_C2 + (j & 1) * L::TILE, c2, f2, p, e[p] & kPiece);
+    for (int p = 0; p < 2; ++p) load_rows<D>(smem + L::OFF_C2 + (j & 1) * L::TILE, c2, f2, p, e[p] & kPiece, t);
     done2 = j + 1;
     // step j - 2 is over: its columns' values and the stage that step j + 1 takes are free
     if (j >= 2 && !mbar_wait(bars.c_empty + stage, (((j - 2) / N1) & 1), a.wait_limit, a.status, abort_flag)) break;
@@ -376,6 +376,33 @@ __device__ __forceinline__ void store_packed(uint32_t taddr, const uint32_t (&r)
   tmem_wait_st();
 }
 
+// A query tile's own rows into TMEM: each warpgroup a part of q's or dout's row.
+template <int D>
+__device__ __forceinline__ void own_rows(const Bars& bars, uint32_t tmem, const AttendGradArgs& a, const Tile& t) {
+  using L = Layout<D, false>;
+  constexpr int PART = D / kGroups;              // 32-bit words: D / 2 a row, two warpgroups a tensor
+  const int wg = threadIdx.x >> 7, row = threadIdx.x & 127, grow = t.tile * BM + row;
+  const GradStride& st = a.st[wg & 1 ? kDout : kQ];
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(wg & 1 ? a.dout : a.q) + t.b * st.b +
+                                                    t.h * st.h + grow * st.n) + (wg >> 1) * (PART / 4);
+  const uint32_t dst = tmem + (static_cast<uint32_t>(row & ~31) << 16) + (wg & 1 ? L::ROWS2 : L::ROWS1) + (wg >> 1) * PART;
+#pragma unroll
+  for (int c = 0; c < PART; c += 16) {
+    uint32_t v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 x = grow < a.N_valid ? __ldg(src + c / 4 + i) : make_uint4(0u, 0u, 0u, 0u);
+      v[4 * i] = x.x;
+      v[4 * i + 1] = x.y;
+      v[4 * i + 2] = x.z;
+      v[4 * i + 3] = x.w;
+    }
+    tmem_st16(dst + c, v);
+  }
+  tmem_wait_st();
+  warp_arrive(bars.r_full, threadIdx.x & 31);
+}
+
 template <int D, bool KEYS, bool MASKED>
 __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_t tmem, const AttendGradArgs& a,
                                         const Tile& t, const uint32_t* entries, float scale_log2, float scale,
@@ -388,30 +415,9 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
   const uint32_t s_col = t_lane + L::S + c0, dp_col = t_lane + L::DP + c0;
   const long long wl = a.wait_limit;
   float neg_lse = 0.f, neg_delta = 0.f;
-  if (!KEYS && t.n_steps > 0) {
+  if (!KEYS) {
     neg_lse = a.neg_lse2[t.bh * a.Npad + grow];
     neg_delta = a.neg_delta[t.bh * a.Npad + grow];
-    // the tile's own rows into TMEM: each warpgroup a part of q's or dout's row
-    constexpr int PART = D / kGroups;              // 32-bit words: D / 2 a row, two warpgroups a tensor
-    const GradStride& st = a.st[wg & 1 ? kDout : kQ];
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(wg & 1 ? a.dout : a.q) + t.b * st.b +
-                                                      t.h * st.h + grow * st.n) + (wg >> 1) * (PART / 4);
-    const uint32_t dst = t_lane + (wg & 1 ? L::ROWS2 : L::ROWS1) + (wg >> 1) * PART;
-#pragma unroll
-    for (int c = 0; c < PART; c += 16) {
-      uint32_t v[16];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 x = grow < a.N_valid ? __ldg(src + c / 4 + i) : make_uint4(0u, 0u, 0u, 0u);
-        v[4 * i] = x.x;
-        v[4 * i + 1] = x.y;
-        v[4 * i + 2] = x.z;
-        v[4 * i + 3] = x.w;
-      }
-      tmem_st16(dst + c, v);
-    }
-    tmem_wait_st();
-    warp_arrive(bars.r_full, lane);
   }
   const uint64_t* sets = reinterpret_cast<const uint64_t*>(smem + L::OFF_SETS);
   bool alive = true;
@@ -523,35 +529,49 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
     tmem_alloc(misc, kTmemCols);
     tmem_relinquish();
   }
+  tc_fence_before();
   __syncthreads();
-  // the tile's kept pieces: the set bits of its blocks' rows, one row for 128-token blocks
-  const int shift = a.block == 128 ? 1 : 0, W = (a.nB + 31) >> 5;
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
   Tile t;
   t.tile = tile;
   t.h = blockIdx.y;
   t.b = blockIdx.z;
   t.bh = static_cast<long long>(t.b) * a.H + t.h;
+  // the tile's own rows do not depend on the tables: they are on their way while
+  // the tables are waited for and the lists counted
+  if (KEYS) {
+    if (threadIdx.x == kProducer * 32) {
+      mbar_arrive_expect_tx(bars.r_full, 2 * L::TILE);
+      for (int p = 0; p < 2; ++p) {
+        load_rows<D>(smem + L::OFF_R1, tk, bars.r_full, p, tile * 2 + p, t);
+        load_rows<D>(smem + L::OFF_R2, tv, bars.r_full, p, tile * 2 + p, t);
+      }
+    }
+  } else if (warp < kProducer) {
+    own_rows<D>(bars, tmem, a, t);
+  }
+  grid_wait();
+  // the tile's kept pieces: the set bits of its blocks' rows, one row for 128-token blocks
+  const int shift = a.block == 128 ? 1 : 0, W = (a.nB + 31) >> 5;
   const uint32_t* rows = KEYS ? a.bits_t : a.bits;
   const int first = shift ? tile : 2 * tile;
   const uint32_t* row0 = rows + (t.bh * a.nB + first) * W;
   const uint32_t* row1 = !shift && first + 1 < a.nB ? row0 + W : nullptr;
   if (threadIdx.x < 128) {
     int n = 0;
-    for (int w = threadIdx.x; w < W; w += 128) n += __popc(__ldg(row0 + w) | (row1 ? __ldg(row1 + w) : 0u));
+    for (int w = threadIdx.x; w < W; w += 128) n += __popc(row0[w] | (row1 ? row1[w] : 0u));
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0 && n) atomicAdd(misc + 2, static_cast<uint32_t>(n));
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = misc[0];
   t.n_steps = ((static_cast<int>(misc[2]) << shift) + 1) >> 1;
   if (warp == kProducer) {
     if (lane == 0) {
       Walk walk;
       walk.init(row0, row1, W, shift, a.N_valid);
-      if (KEYS) produce<D, KEYS, MASKED>(smem, bars, tk, tv, tq, tdo, a, t, walk, entries, abort_flag);
-      else produce<D, KEYS, MASKED>(smem, bars, tq, tdo, tk, tv, a, t, walk, entries, abort_flag);
+      if (KEYS) produce<D, KEYS, MASKED>(smem, bars, tq, tdo, a, t, walk, entries, abort_flag);
+      else produce<D, KEYS, MASKED>(smem, bars, tk, tv, a, t, walk, entries, abort_flag);
     }
   } else if (warp == kIssuer) {
     issue<D, KEYS>(smem, bars, tmem, a, t.n_steps, abort_flag);
@@ -572,7 +592,7 @@ attend_grad_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                       const __grid_constant__ AttendGradArgs a, int tiles, float scale_log2, float scale) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  // a CTA of this launch already gave up on a wait: skip the work, the call has failed
+  // a CTA already gave up on a wait: skip the work, the call has failed
   if (*reinterpret_cast<volatile int32_t*>(a.status) == LBSA_ERR_TIMEOUT) return;
   if (static_cast<int>(blockIdx.x) < tiles) run_tile<D, true, MASKED>(smem, &tq, &tk, &tv, &tdo, a, blockIdx.x, scale_log2, scale);
   else run_tile<D, false, MASKED>(smem, &tq, &tk, &tv, &tdo, a, blockIdx.x - tiles, scale_log2, scale);
@@ -587,16 +607,14 @@ cudaError_t launch_attend_grad_tc(const CUtensorMap* tq, const CUtensorMap* tk, 
   auto go = [&](auto kern, int smem) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(2 * tiles, a.H, a.B), kThreads, smem, s>>>(*tq, *tk, *tv, *tdo, a, tiles,
-                                                          static_cast<float>(1.4426950408889634 * scale),
-                                                          static_cast<float>(scale));
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(2 * tiles, a.H, a.B), dim3(kThreads), smem, s, *tq, *tk, *tv, *tdo, a, tiles,
+                            static_cast<float>(1.4426950408889634 * scale), static_cast<float>(scale));
   };
   if (a.d == 128)
-    return a.masks ? go(attend_grad_tc_kernel<128, true>, Layout<128, true>::BYTES)
-                   : go(attend_grad_tc_kernel<128, false>, Layout<128, true>::BYTES);
-  return a.masks ? go(attend_grad_tc_kernel<64, true>, Layout<64, true>::BYTES)
-                 : go(attend_grad_tc_kernel<64, false>, Layout<64, true>::BYTES);
+    return a.masks ? go(attend_grad_tc_kernel<128, true>, kSmemBytes<128>)
+                   : go(attend_grad_tc_kernel<128, false>, kSmemBytes<128>);
+  return a.masks ? go(attend_grad_tc_kernel<64, true>, kSmemBytes<64>)
+                 : go(attend_grad_tc_kernel<64, false>, kSmemBytes<64>);
 }
 
 }  // namespace lbsa

@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
     tok = next_tok;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  grid_launch_dependents();
   if (!norm) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[group * D + lane * 8 + j] = acc[j];
@@ -422,10 +423,11 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const __grid_constant
   // the units' partial rows lie together: all of the item's, or (one head a unit) one run a batch element
   const long long run = shared ? static_cast<long long>(a.chunk_end[item] - first) * gx : gx;
   double t = 0.0;
+  grid_wait();
   for (int b = 0; b < (shared ? 1 : B); ++b) {
     const float* p = a.partial + static_cast<long long>(first + (shared ? 0 : b * it.H + row)) * gx * a.d + e;
 #pragma unroll 8
-    for (long long i = threadIdx.y; i < run; i += 32) t += __ldg(p + i * a.d);
+    for (long long i = threadIdx.y; i < run; i += 32) t += p[i * a.d];
   }
   sum[threadIdx.y][threadIdx.x] = t;
   __syncthreads();
@@ -544,8 +546,7 @@ cudaError_t launch_norm_rope_backward(const RopeItem* items, int count, int B, i
   int rows = 0;
   for (int i = 0; i < count; ++i) rows += items[i].weight ? items[i].weight_heads : 0;
   if (e != cudaSuccess || rows == 0) return e;
-  weight_grad_kernel<<<dim3(d / 32, rows), dim3(32, 32), 0, s>>>(a, gx, B);
-  return cudaGetLastError();
+  return launch_dependent(weight_grad_kernel, dim3(d / 32, rows), dim3(32, 32), 0, s, a, gx, B);
 }
 
 cudaError_t launch_rope_table(const RopePos& pos, double theta, const double* start, float* table, cudaStream_t s) {
