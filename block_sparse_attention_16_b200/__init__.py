@@ -376,26 +376,33 @@ def lbsa_attend_backward(q, k, v, bs: Blockset, out, lse, dout, dq=None, dk=None
     (want_lse=True) and the gradient dout of out.  The tensors share q's shape
     and dtype, their strides may differ (new gradients take those of q, k and
     v).  The same inputs give the same bits on every call."""
-    desc = _desc(q)
-    dq, dk, dv = (torch.empty_like(x) if t is None else t for x, t in ((q, dq), (k, dk), (v, dv)))
-    tensors = (q, k, v, out, dout, dq, dk, dv)
+    if q.dim() != 4:
+        raise LbsaError(LBSA_ERR_INVALID_ARG, "expected [B, H, N, d] tensors")
     shape, dtype, device = q.shape, q.dtype, q.get_device()
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise LbsaError(LBSA_ERR_UNSUPPORTED, f"dtype {dtype}")
+    if device < 0 or device != torch.cuda.current_device():
+        _on_device(q, "q", contiguous=False)
     B, H, N, d = shape
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
     strides = []
-    for t in tensors:
+    for t in (q, k, v, out, dout, dq, dk, dv):
         st = t.stride()
         if t.shape != shape or t.dtype is not dtype or t.get_device() != device or st[3] != 1:
             raise LbsaError(LBSA_ERR_INVALID_ARG, "q, k, v, out, dout and the gradients must share shape, dtype and "
                                                   "device, with a contiguous last dim")
-        # the stride of a dimension of one entry means nothing
-        strides += st[:3] if B > 1 and H > 1 and N > 1 else [a if size > 1 else d for a, size in zip(st, shape)][:3]
+        strides += st[:3]
     if lse is None:
         raise LbsaError(LBSA_ERR_INVALID_ARG, "lse is needed (lbsa_attend with want_lse=True)")
-    _on_device(lse, "lse", torch.float32, B * H * N)
-    desc.stride_b, desc.stride_h, desc.stride_n = strides[0:3]
+    if not _fits(lse, device, torch.float32, B * H * N):
+        _on_device(lse, "lse", torch.float32, B * H * N)
+    desc = _Desc(B, H, N, d, 0 if dtype is torch.bfloat16 else 1, 0, *strides[:3])
+    stream = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
     _check(load_library().lbsa_attend_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
                                                lse.data_ptr(), ctypes.byref(desc), _PACK_STRIDES(*strides), bs.handle,
-                                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _stream(stream)))
+                                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), stream))
     return dq, dk, dv
 
 
@@ -549,61 +556,70 @@ _PACK_POS = struct.Struct("Q8i").pack               # _RopePos
 assert struct.calcsize("5Q4i9q") == ctypes.sizeof(_RopeItem) and struct.calcsize("Q8i") == ctypes.sizeof(_RopePos)
 
 
-def _rope_call(xs, ys, dys, weights, dweights, table, grid, dims, layout, perm):
-    """The arguments that lbsa_rope, lbsa_norm_rope and lbsa_norm_rope_backward share."""
+def _fits(t, device: int, dtype, numel: int) -> bool:
+    return t.get_device() == device and t.dtype is dtype and t.is_contiguous() and t.numel() >= numel
+
+
+def _rope_call(xs, ys, dys, weights, dweights, table, grid, dims, layout, perm, stream):
+    """The arguments that lbsa_rope, lbsa_norm_rope and lbsa_norm_rope_backward
+    share, and the stream.  ys None: new outputs, laid out as their inputs."""
     n = len(xs)
-    if not 1 <= n <= 3 or len(ys) != n or len(weights) != n or (dys is not None and len(dys) != n):
+    if not 1 <= n <= 3 or len(weights) != n or (ys is not None and len(ys) != n) or (dys is not None and len(dys) != n):
         raise LbsaError(LBSA_ERR_INVALID_ARG, "need 1..3 tensors, with as many weights (None: no norm), outputs and gradients")
     first = xs[0]
     if first.dim() != 4:
         raise LbsaError(LBSA_ERR_INVALID_ARG, "expected [B, H, N, d] tensors")
     B, _, N, d = first.shape
-    dtype = first.dtype
+    dtype, device = first.dtype, first.get_device()
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise LbsaError(LBSA_ERR_UNSUPPORTED, f"dtype {dtype}")
-    _on_device(first, "x", contiguous=False)
-    device = first.get_device()
-    packed = b""
+    if device < 0 or device != torch.cuda.current_device():
+        _on_device(first, "x", contiguous=False)
+    outs, packed = [], b""
     for i, x in enumerate(xs):
+        y = torch.empty_like(x) if ys is None else ys[i]
+        outs.append(y)
+        dy = x if dys is None else dys[i]
         shape = x.shape
-        H = shape[1]
-        if len(shape) != 4 or shape[0] != B or shape[2] != N or shape[3] != d:
-            raise LbsaError(LBSA_ERR_INVALID_ARG, "tensors of one call must share B, N, d and dtype")
-        strides = []
-        for t in ((x, ys[i]) if dys is None else (x, ys[i], dys[i])):
-            if t.get_device() != device or t.dtype is not dtype:
+        for t in (x, y, dy):
+            if t.get_device() != device or t.dtype is not dtype or t.dim() != 4:
                 _on_device(t, "a tensor of the call", dtype, contiguous=False)
-            st = t.stride()
-            if t.shape != shape or st[3] != 1:
-                raise LbsaError(LBSA_ERR_INVALID_ARG, "tensors of one call must share B, N, d and dtype, outputs and "
-                                                      "gradients their input's shape, with a contiguous last dim")
-            # the stride of a dimension of one entry means nothing
-            strides += st[:3] if B > 1 and H > 1 and N > 1 else [a if size > 1 else d for a, size in zip(st, shape)][:3]
-        if dys is None:
-            strides += (d, d, d)
+                raise LbsaError(LBSA_ERR_INVALID_ARG, "expected [B, H, N, d] tensors")
+        x0, x1, x2, x3 = x.stride()
+        y0, y1, y2, y3 = y.stride()
+        g0, g1, g2, g3 = (x0, x1, x2, x3) if dys is None else dy.stride()
+        H = shape[1]
+        if (shape[0] != B or shape[2] != N or shape[3] != d or (ys is not None and y.shape != shape)
+                or (dys is not None and dy.shape != shape) or x3 != 1 or y3 != 1 or g3 != 1):
+            raise LbsaError(LBSA_ERR_INVALID_ARG, "tensors of one call must share B, N and d, outputs and gradients have "
+                                                  "their input's shape, all with a contiguous last dim")
         w, wp, dwp, wt, wh = weights[i], 0, 0, 0, 1
         if w is not None:
-            if w.get_device() != device or not w.is_contiguous():
-                _on_device(w, "weight")
-            if w.dtype not in (torch.bfloat16, torch.float32) or w.shape not in ((d,), (H, d)):
+            wt = 0 if w.dtype is torch.bfloat16 else 1
+            if not _fits(w, device, torch.float32 if wt else torch.bfloat16, 0):
+                _on_device(w, "weight", torch.float32 if wt else torch.bfloat16)
+            if w.shape != (d,) and w.shape != (H, d):
                 raise LbsaError(LBSA_ERR_INVALID_ARG, "a weight is bf16 or fp32, [d] or [H, d]")
-            wp, wt = w.data_ptr(), 0 if w.dtype is torch.bfloat16 else 1
+            wp = w.data_ptr()
             wh = 1 if w.dim() == 1 else H
             dwp = dweights[i].data_ptr() if dweights else 0
-        packed += _PACK_ITEM(x.data_ptr(), ys[i].data_ptr(), 0 if dys is None else dys[i].data_ptr(), wp, dwp, H,
-                             w is not None or dweights is None, wt, wh, *strides)
+        packed += _PACK_ITEM(x.data_ptr(), y.data_ptr(), dy.data_ptr(), wp, dwp, H, w is not None or dweights is None, wt,
+                             wh, x0, x1, x2, y0, y1, y2, g0, g1, g2)
     pos = None
     if table is not None:
-        if grid is None or dims is None or layout not in _ROPE_LAYOUTS:
-            raise LbsaError(LBSA_ERR_INVALID_ARG, 'a rotation needs grid, dims and layout "interleaved" or "half"')
-        if len(grid) != 3 or len(dims) != 3:
-            raise LbsaError(LBSA_ERR_INVALID_ARG, "grid and dims must have three entries (time, height, width)")
-        _on_device(table, "table", torch.float32, max(sum(e * r for e, r in zip(grid, dims)), 0))
+        if grid is None or dims is None or layout not in _ROPE_LAYOUTS or len(grid) != 3 or len(dims) != 3:
+            raise LbsaError(LBSA_ERR_INVALID_ARG, 'a rotation needs grid and dims (time, height, width) and layout '
+                                                  '"interleaved" or "half"')
+        need = max(grid[0] * dims[0] + grid[1] * dims[1] + grid[2] * dims[2], 0)
+        if not _fits(table, device, torch.float32, need):
+            _on_device(table, "table", torch.float32, need)
         pos = _PACK_POS(table.data_ptr(), *grid, *dims, _ROPE_LAYOUTS[layout], 0)
     if perm is not None:
-        _on_device(perm, "perm", torch.int32, N)
+        if not _fits(perm, device, torch.int32, N):
+            _on_device(perm, "perm", torch.int32, N)
         perm = perm.data_ptr()
-    return packed, n, B, N, d, 0 if dtype is torch.bfloat16 else 1, pos, perm
+    stream = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    return outs, (packed, n, B, N, d, 0 if dtype is torch.bfloat16 else 1, pos, perm), stream
 
 
 def lbsa_rope(xs, table, grid, dims, perm=None, inverse: bool = False, layout: str = "interleaved", outs=None,
@@ -614,10 +630,8 @@ def lbsa_rope(xs, table, grid, dims, perm=None, inverse: bool = False, layout: s
     sum(dims) stay as they are.  With perm (lbsa_partition_perm) the rows move
     into block order in the same pass; inverse=True rotates back and scatters
     the rows back, which is also the gradient."""
-    xs = list(xs)
-    outs = [torch.empty_like(x) for x in xs] if outs is None else list(outs)
-    args = _rope_call(xs, outs, None, [None] * len(xs), None, table, grid, dims, layout, perm)
-    _check(load_library().lbsa_rope(*args, int(inverse), _stream(stream)))
+    outs, args, stream = _rope_call(xs, outs, None, (None,) * len(xs), None, table, grid, dims, layout, perm, stream)
+    _check(load_library().lbsa_rope(*args, bool(inverse), stream))
     return outs
 
 
@@ -627,10 +641,8 @@ def lbsa_norm_rope(xs, weights, table=None, grid=None, dims=None, perm=None, eps
     their rotation (as lbsa_rope; without a table none) and the move into block
     order, in one pass over 1..3 tensors [B, H_i, N, d].  A weight is [d] or
     [H_i, d]; a tensor whose weight is None (values) is only moved."""
-    xs = list(xs)
-    outs = [torch.empty_like(x) for x in xs] if outs is None else list(outs)
-    args = _rope_call(xs, outs, None, list(weights), (), table, grid, dims, layout, perm)
-    _check(load_library().lbsa_norm_rope(*args, float(eps), _stream(stream)))
+    outs, args, stream = _rope_call(xs, outs, None, weights, (), table, grid, dims, layout, perm, stream)
+    _check(load_library().lbsa_norm_rope(*args, float(eps), stream))
     return outs
 
 
@@ -639,11 +651,9 @@ def lbsa_norm_rope_backward(dys, xs, weights, table=None, grid=None, dims=None, 
     """Gradients of lbsa_norm_rope from those of its outputs (dys, in block order)
     and its inputs: (dxs in source order, dweights fp32 with None where there is
     no weight).  The same inputs give the same bits on every call."""
-    xs, weights = list(xs), list(weights)
-    dxs = [torch.empty_like(x) for x in xs] if dxs is None else list(dxs)
-    dws = [None if w is None else torch.empty(w.shape, dtype=torch.float32, device=w.device) for w in weights]
-    args = _rope_call(xs, dxs, list(dys), weights, dws, table, grid, dims, layout, perm)
-    _check(load_library().lbsa_norm_rope_backward(*args, float(eps), _stream(stream)))
+    dws = [None if w is None else torch.empty_like(w, dtype=torch.float32) for w in weights]
+    dxs, args, stream = _rope_call(xs, dxs, dys, weights, dws, table, grid, dims, layout, perm, stream)
+    _check(load_library().lbsa_norm_rope_backward(*args, float(eps), stream))
     return dxs, dws
 
 

@@ -223,6 +223,13 @@ int rope_pos(const lbsa_rope_pos* p, int d, lbsa::RopePos* out) {
   return LBSA_OK;
 }
 
+// the stride of a dimension of one entry means nothing: it becomes a row
+void plain_strides(int64_t (&st)[3], int B, int H, int N, int d) {
+  if (B == 1) st[0] = d;
+  if (H == 1) st[1] = d;
+  if (N == 1) st[2] = d;
+}
+
 int rope_tensor(const void* p, const char* name, const int64_t (&st)[3], int d, int es) {
   int rc;
   if ((rc = validate_ptr(p, name)) != LBSA_OK) return rc;
@@ -245,7 +252,10 @@ int rope_items(const lbsa_rope_item* items, int count, int B, int N, int d, int 
   const int es = dtype == LBSA_BF16 ? 2 : 4;
   long long heads = 0;
   for (int i = 0; i < count; ++i) {
-    const lbsa_rope_item& a = items[i];
+    lbsa_rope_item a = items[i];
+    plain_strides(a.x_stride, B, a.H, N, d);
+    plain_strides(a.y_stride, B, a.H, N, d);
+    plain_strides(a.dy_stride, B, a.H, N, d);
     if (a.H < 1) return fail(LBSA_ERR_INVALID_ARG, "H must be >= 1 (got %d)", a.H);
     if ((rc = rope_tensor(a.y, backward ? "dx" : "y", a.y_stride, d, es)) != LBSA_OK) return rc;
     if ((!backward || a.weight) && (rc = rope_tensor(a.x, "x", a.x_stride, d, es)) != LBSA_OK) return rc;
@@ -640,6 +650,12 @@ int lbsa_attend_backward(const void* q, const void* k, const void* v, const void
                          const float* lse, const lbsa_qkv_desc* desc, const int64_t* strides,
                          const lbsa_blockset* bs, void* dq, void* dk, void* dv, void* stream) {
   int rc;
+  lbsa_qkv_desc own;
+  if (desc && strides) {       // desc's strides are not used then
+    own = *desc;
+    own.stride_b = own.stride_h = own.stride_n = own.d;
+    desc = &own;
+  }
   if (desc)
     log_line("lbsa_attend_backward B=%d H=%d N=%d d=%d dtype=%d blockset=%p (scope %d)", desc->B, desc->H, desc->N_valid,
              desc->d, desc->dtype, static_cast<const void*>(bs), bs ? bs->scope : -1);
@@ -651,14 +667,17 @@ int lbsa_attend_backward(const void* q, const void* k, const void* v, const void
     if ((rc = validate_ptr(i < 5 ? ins[i] : outs[i - 5], names[i])) != LBSA_OK) return rc;
   lbsa::GradStride st[lbsa::kGradTensors];
   for (int i = 0; i < lbsa::kGradTensors; ++i) {
-    lbsa_qkv_desc one = *desc;
+    int64_t v[3] = {desc->stride_b, desc->stride_h, desc->stride_n};
     if (strides) {
-      one.stride_b = strides[3 * i];
-      one.stride_h = strides[3 * i + 1];
-      one.stride_n = strides[3 * i + 2];
+      for (int j = 0; j < 3; ++j) v[j] = strides[3 * i + j];
+      plain_strides(v, desc->B, desc->H, desc->N_valid, desc->d);
+      lbsa_qkv_desc one = *desc;
+      one.stride_b = v[0];
+      one.stride_h = v[1];
+      one.stride_n = v[2];
       if ((rc = validate_desc(&one)) != LBSA_OK) return rc;
     }
-    st[i] = lbsa::GradStride{one.stride_b, one.stride_h, one.stride_n};
+    st[i] = lbsa::GradStride{v[0], v[1], v[2]};
   }
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return fail(LBSA_ERR_INVALID_ARG, "lse is NULL or not 4-byte aligned");

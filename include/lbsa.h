@@ -266,7 +266,8 @@ int lbsa_attend(const void* q, const void* k, const void* v, const lbsa_qkv_desc
  *   dq, dk, dv out: gradients, dtype of q; may alias nothing
  *   strides    host [8][3]: element strides (batch, head, row) of q, k, v, out,
  *              dout, dq, dk, dv in place of desc's (the gradient of a
- *              layer's output seldom has q's), or NULL: all have desc's
+ *              layer's output seldom has q's), or NULL: all have desc's.  The
+ *              stride of a dimension of one entry is ignored
  * With P the probabilities
  * of the kept pairs, D_r = sum_e dout_re out_re and dS = P (dout v^T - D):
  * dv = P^T dout, dq = dS k / sqrt(d), dk = dS^T q / sqrt(d).  A row that keeps
@@ -383,8 +384,9 @@ typedef struct {
 } lbsa_rope_pos;
 
 /* One tensor [B, H, N, d] of a call; strides in elements, the d stride is 1;
- * base pointers and byte strides are multiples of 16.  Tensors of one call may
- * differ in H (shared key heads) and strides. */
+ * base pointers and byte strides are multiples of 16 (the stride of a dimension
+ * of one entry is ignored).  Tensors of one call may differ in H (shared key
+ * heads) and strides. */
 typedef struct {
   const void* x;                /* input                                            */
   void* y;                      /* output; backward: the gradient of x              */

@@ -34,8 +34,14 @@ def test_desc_is_checked(desc, code):
 def test_strides_are_checked(tensor, at, value):
     strides = [2 * 256 * 64, 256 * 64, 64] * 8
     strides[3 * tensor + at] = value
-    assert _call(strides=strides) == INV
+    assert _call(dict(B=2), strides=strides) == INV
     assert "stride" in lbsa.lbsa_last_error()
+
+
+def test_strides_of_single_entries_are_ignored():
+    # the batch stride means nothing with B = 1: the call gets as far as the missing blockset
+    assert _call(strides=[0, 256 * 64, 64] * 8) == INV
+    assert "blockset" in lbsa.lbsa_last_error()
 
 
 @pytest.mark.parametrize("name", NAMES)

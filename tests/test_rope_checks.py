@@ -52,7 +52,7 @@ def test_positions_are_checked(name, kw, code):
 ])
 @pytest.mark.parametrize("name", ["lbsa_norm_rope", "lbsa_norm_rope_backward"])
 def test_tensors_are_checked(name, kw):
-    assert _call(name, _item(**kw), _pos()) == INV
+    assert _call(name, _item(**kw), _pos(), B=2) == INV
 
 
 @pytest.mark.parametrize("kw", [dict(dy=0), dict(dy=2 * A), dict(dy=A + 4), dict(dweight=0),
