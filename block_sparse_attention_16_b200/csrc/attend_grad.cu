@@ -17,7 +17,7 @@
 // 128-row tiles (a row that keeps nothing, or does not exist, gets -inf and 0,
 // so that its P is 0 without a test), and the kept pairs as bits in
 // both directions; the per-token sets go to [key block][query block].
-#include "lbsa_device.cuh"
+#include "lbsa_train_device.cuh"
 
 namespace lbsa {
 namespace {

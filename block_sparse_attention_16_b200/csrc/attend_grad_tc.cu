@@ -26,7 +26,7 @@
 // operand from TMEM.  With both operands in shared memory a 128 x 128 x 16
 // product reads 8 KB in the 64 cycles that the tensor core needs for it, the
 // whole bandwidth, and took 90 to 100 cycles.
-#include "lbsa_device.cuh"
+#include "lbsa_train_device.cuh"
 
 namespace lbsa {
 namespace {

@@ -12,6 +12,7 @@
 
 #include "lbsa_device.cuh"
 #include "lbsa_routed.h"
+#include "lbsa_train.h"
 
 namespace {
 

@@ -20,7 +20,7 @@
 // element): a token's position, perm entry and (cos, sin) are looked up once
 // for its heads, the weight once for the block, and the next rows' loads are in
 // flight while a batch of rows is worked on.
-#include "lbsa_device.cuh"
+#include "lbsa_train_device.cuh"
 
 namespace lbsa {
 namespace {
