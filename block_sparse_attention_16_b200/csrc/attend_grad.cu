@@ -123,62 +123,107 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
 
 // ------------------------------------------------------------------ CUDA cores
 // A CTA owns R rows (keys, or queries) and walks the 64-row pieces of the
-// other side that its block is kept with.  256 threads as 16 x 16: thread
-// (ty, tx) computes S and dP for rows ty + 16 i and columns tx + 16 j, then,
-// P and dS in shared memory, its R / 16 rows x d / 16 columns of the sums.
-// Bound by shared-memory reads and FMA issue in about equal parts: at R = 64 a
-// thread reads 8 vectors for 64 FMAs.  R = 64 wherever that fills the SMs; with
-// fewer rows R = 32 or 16 spreads them over more CTAs (256 tokens, 2 heads of
-// 64, 60 % of the blocks: 55 us with R = 64).
+// other side that its block is kept with.  256 threads as R / 4 x 16 x 64 / R:
+// thread (ty, tx, kz) computes S and dP for rows ty + R / 4 i and columns
+// tx + 16 j over its share of the elements (the 64 / R threads of a share sum
+// by shuffles), then, P and dS in shared memory, 4 rows x d / 16 columns of the
+// sums over its share of the piece's rows.
+// Bound by shared-memory reads: 4 x 4 results a thread take 8 vectors for 64
+// FMAs, twice the reads that FMA issue would cover.  R = 64 wherever that fills
+// the SMs; with fewer rows R = 32 or 16 spreads them over more CTAs.
 constexpr int kPitch = 68;        // floats a row of P and dS: 16-byte rows, no bank conflicts
 
+// Rows r0 .. of a tensor into shared memory, zeros past N; cp.async, not waited for.
 template <int D>
 __device__ __forceinline__ void load_rows(float* s, const float* g, long long stride, int r0, int rows, int N) {
   for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
     const int r = i / (D / 4), e = (i - r * (D / 4)) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < N) v = __ldg(reinterpret_cast<const float4*>(g + (r0 + r) * stride + e));
-    *reinterpret_cast<float4*>(s + r * (D + 4) + e) = v;
+    const bool in = r0 + r < N;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(s + r * (D + 4) + e)),
+                 "l"(g + (in ? r0 + r : 0) * stride + e), "r"(in ? 16 : 0)
+                 : "memory");
   }
 }
+__device__ __forceinline__ void loads_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void loads_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-// acc[i][j] = row ty + 16 i of x  .  row tx + 16 j of y
-template <int D, int RI>
-__device__ __forceinline__ void dots(float (&acc)[RI][4], const float* x, const float* y, int ty, int tx) {
+// The 64-row pieces that a block is kept with, ascending.
+struct Pieces {
+  const uint32_t* list;
+  int W, N, shift, w, sub;
+  uint32_t word;
+  int other, c0;                // the piece's block and first row
+  __device__ __forceinline__ bool next() {
+    if (sub > 0 && sub <= shift && (other << shift) * 64 + sub * 64 < N) {      // the block's other half
+      c0 = (other << shift) * 64 + sub * 64;
+      ++sub;
+      return true;
+    }
+    while (word == 0u) {
+      if (++w >= W) return false;
+      word = list[w];
+    }
+    other = w * 32 + __ffs(word) - 1;
+    word &= word - 1u;
+    c0 = (other << shift) * 64;
+    sub = 1;
+    return true;
+  }
+};
+
+template <int KS>
+__device__ __forceinline__ float sum_shares(float v) {
 #pragma unroll
-  for (int i = 0; i < RI; ++i)
+  for (int o = 1; o < KS; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// acc[i][j] = row ty + R / 4 i of x  .  row tx + 16 j of y
+template <int D, int R>
+__device__ __forceinline__ void dots(float (&acc)[4][4], const float* x, const float* y, int ty, int tx, int kz) {
+  constexpr int KS = 64 / R;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll 4
-  for (int e = 0; e < D; e += 4) {
-    float4 xr[RI], yr[4];
+  for (int e = 4 * kz; e < D; e += 4 * KS) {
+    float4 xr[4], yr[4];
 #pragma unroll
-    for (int i = 0; i < RI; ++i) xr[i] = *reinterpret_cast<const float4*>(x + (ty + 16 * i) * (D + 4) + e);
+    for (int i = 0; i < 4; ++i) {
+      xr[i] = *reinterpret_cast<const float4*>(x + (ty + R / 4 * i) * (D + 4) + e);
+      yr[i] = *reinterpret_cast<const float4*>(y + (tx + 16 * i) * (D + 4) + e);
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) yr[i] = *reinterpret_cast<const float4*>(y + (tx + 16 * i) * (D + 4) + e);
-#pragma unroll
-    for (int i = 0; i < RI; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         acc[i][j] = fmaf(xr[i].x, yr[j].x, fmaf(xr[i].y, yr[j].y, fmaf(xr[i].z, yr[j].z, fmaf(xr[i].w, yr[j].w, acc[i][j]))));
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = sum_shares<KS>(acc[i][j]);
 }
 
-// acc[i][.] += sum_c w[ty + 16 i][c] y[c][columns of tx]
-template <int D, int RI>
-__device__ __forceinline__ void weighted(float (&acc)[RI][D / 16], const float* w, const float* y, int ty, int tx) {
-#pragma unroll 4
-  for (int c = 0; c < 64; c += 4) {
-    float4 wr[RI];
+// acc[i][.] += sum of w[ty + R / 4 i][c] y[c][columns of tx] over the thread's share of the c
+template <int D, int R>
+__device__ __forceinline__ void weighted(float (&acc)[4][D / 16], const float* w, const float* y, int ty, int tx, int kz) {
+#pragma unroll 2
+  for (int c = 4 * kz; c < 64; c += 4 * (64 / R)) {
+    float4 wr[4];
 #pragma unroll
-    for (int i = 0; i < RI; ++i) wr[i] = *reinterpret_cast<const float4*>(w + (ty + 16 * i) * kPitch + c);
+    for (int i = 0; i < 4; ++i) wr[i] = *reinterpret_cast<const float4*>(w + (ty + R / 4 * i) * kPitch + c);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
       for (int g = 0; g < D / 64; ++g) {
         const float4 v = *reinterpret_cast<const float4*>(y + (c + k) * (D + 4) + g * 64 + tx * 4);
 #pragma unroll
-        for (int i = 0; i < RI; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const float p = k == 0 ? wr[i].x : k == 1 ? wr[i].y : k == 2 ? wr[i].z : wr[i].w;
           acc[i][g * 4 + 0] = fmaf(p, v.x, acc[i][g * 4 + 0]);
           acc[i][g * 4 + 1] = fmaf(p, v.y, acc[i][g * 4 + 1]);
@@ -190,35 +235,40 @@ __device__ __forceinline__ void weighted(float (&acc)[RI][D / 16], const float* 
   }
 }
 
-template <int D, int RI>
-__device__ __forceinline__ void store_rows(float* g, long long stride, int r0, int N, const float (&acc)[RI][D / 16],
-                                           float f, int ty, int tx) {
+// the shares' sums; each of a share's threads stores some of the rows
+template <int D, int R>
+__device__ __forceinline__ void store_rows(float* g, long long stride, int r0, int N, const float (&acc)[4][D / 16], float f,
+                                           int ty, int tx, int kz) {
+  constexpr int KS = 64 / R;
 #pragma unroll
-  for (int i = 0; i < RI; ++i) {
-    const int r = r0 + ty + 16 * i;
-    if (r >= N) continue;
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + ty + R / 4 * i;
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c)
-      *reinterpret_cast<float4*>(g + r * stride + c * 64 + tx * 4) =
-          make_float4(acc[i][c * 4] * f, acc[i][c * 4 + 1] * f, acc[i][c * 4 + 2] * f, acc[i][c * 4 + 3] * f);
+    for (int c = 0; c < D / 64; ++c) {
+      float4 v;
+      v.x = sum_shares<KS>(acc[i][c * 4]) * f;
+      v.y = sum_shares<KS>(acc[i][c * 4 + 1]) * f;
+      v.z = sum_shares<KS>(acc[i][c * 4 + 2]) * f;
+      v.w = sum_shares<KS>(acc[i][c * 4 + 3]) * f;
+      if (r < N && i / (4 / KS) == kz) *reinterpret_cast<float4*>(g + r * stride + c * 64 + tx * 4) = v;
+    }
   }
 }
 
+// The next piece's rows are on their way while one is worked on, wherever two
+// buffers fit (all but d = 128, R = 64).
 template <int D, int R>
-constexpr int f32_smem() { return (2 * (R + 64) * (D + 4) + 2 * R * kPitch) * 4; }
+constexpr int kF32Buffers = D == 128 && R == 64 ? 1 : 2;
+template <int D, int R>
+constexpr int f32_smem() { return ((2 * R + kF32Buffers<D, R> * 2 * 64) * (D + 4) + 2 * R * kPitch) * 4; }
 
-// blockIdx.x: tiles of keys (dk, dv), then tiles of queries (dq).
-template <int D, int R>
-__global__ void __launch_bounds__(256) attend_grad_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
-                                                             const float* __restrict__ v, const float* __restrict__ dout,
-                                                             const __grid_constant__ AttendGradArgs a, int tiles) {
-  extern __shared__ __align__(16) float sm[];
-  constexpr int RI = R / 16;
-  float *r1 = sm, *r2 = r1 + R * (D + 4), *c1 = r2 + R * (D + 4), *c2 = c1 + 64 * (D + 4), *sp = c2 + 64 * (D + 4),
-        *sd = sp + R * kPitch;
-  const bool keys = blockIdx.x < tiles;
-  const int tile = keys ? blockIdx.x : blockIdx.x - tiles;
-  const int h = blockIdx.y, b = blockIdx.z, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+template <int D, int R, bool keys>
+__device__ __forceinline__ void f32_tile(float* sm, const float* q, const float* k, const float* v, const float* dout,
+                                         const AttendGradArgs& a, int tile) {
+  constexpr int KS = 64 / R, NB = kF32Buffers<D, R>, PIECE = 64 * (D + 4);
+  float *r1 = sm, *r2 = r1 + R * (D + 4), *cs = r2 + R * (D + 4), *sp = cs + NB * 2 * PIECE, *sd = sp + R * kPitch;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int kz = threadIdx.x % KS, tx = threadIdx.x / KS % 16, ty = threadIdx.x / (KS * 16);
   const int N = a.N_valid, shift = a.block == 128 ? 1 : 0, W = (a.nB + 31) >> 5;
   const long long bh = static_cast<long long>(b) * a.H + h;
   const GradStride &s_r1 = a.st[keys ? kK : kQ], &s_r2 = a.st[keys ? kV : kDout];
@@ -231,51 +281,84 @@ __global__ void __launch_bounds__(256) attend_grad_f32_kernel(const float* __res
   const float scale = 1.0f / sqrtf(static_cast<float>(D)), scale2 = scale * kLog2e;
   load_rows<D>(r1, (keys ? k : q) + offset(s_r1, b, h, 0), s_r1.n, r0, R, N);
   load_rows<D>(r2, (keys ? v : dout) + offset(s_r2, b, h, 0), s_r2.n, r0, R, N);
-  float acc1[RI][D / 16], acc2[RI][D / 16];
+  float acc1[4][D / 16], acc2[4][D / 16];
 #pragma unroll
-  for (int i = 0; i < RI; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) acc1[i][j] = acc2[i][j] = 0.f;
   grid_wait();
-  const uint32_t* list = (keys ? a.bits_t : a.bits) + (bh * a.nB + mine) * W;
-  for (int w = 0; w < W; ++w) {
-    for (uint32_t word = list[w]; word; word &= word - 1) {
-      const int other = w * 32 + __ffs(word) - 1;
-      uint64_t set = ~0ull;       // per-token lists: the query tokens that keep the key block
-      if (a.masks) set = a.masks_t[(bh * a.nB + (keys ? mine : other)) * a.nB + (keys ? other : mine)];
-      for (int s = 0; s <= shift; ++s) {
-        const int c0 = (other << shift) * 64 + s * 64;
-        if (c0 >= N) break;
-        __syncthreads();          // the last piece's sums are done with c1, c2, sp, sd
-        load_rows<D>(c1, g1, s_c1.n, c0, 64, N);
-        load_rows<D>(c2, g2, s_c2.n, c0, 64, N);
-        __syncthreads();
-        float p[RI][4], g[RI][4];
-        dots<D, RI>(p, r1, c1, ty, tx);
-        dots<D, RI>(g, r2, c2, ty, tx);
+  auto load = [&](int buf, int c0) {
+    load_rows<D>(cs + buf * 2 * PIECE, g1, s_c1.n, c0, 64, N);
+    load_rows<D>(cs + buf * 2 * PIECE + PIECE, g2, s_c2.n, c0, 64, N);
+    loads_commit();
+  };
+  Pieces it{(keys ? a.bits_t : a.bits) + (bh * a.nB + mine) * W, W, N, shift, -1, 0, 0u, 0, 0};
+  bool more = it.next();
+  if (more) load(0, it.c0);
+  float nl[4], nd[4];               // -lse, -D: of the thread's columns (keys) or rows (queries)
+  if (!keys) {
 #pragma unroll
-        for (int i = 0; i < RI; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int row = ty + 16 * i, col = tx + 16 * j;
-            const int qn = keys ? c0 + col : r0 + row, kn = keys ? r0 + row : c0 + col;
-            const bool on = kn < N && ((set >> (qn & 63)) & 1ull);     // qn < Npad: the tables are padded
-            const float pr = on ? exp2f(fmaf(p[i][j], scale2, neg_lse2[qn])) : 0.f;
-            sp[row * kPitch + col] = pr;
-            sd[row * kPitch + col] = on ? pr * (g[i][j] + neg_delta[qn]) : 0.f;
-          }
-        __syncthreads();
-        weighted<D, RI>(acc1, sd, c1, ty, tx);
-        if (keys) weighted<D, RI>(acc2, sp, c2, ty, tx);
-      }
+    for (int i = 0; i < 4; ++i) {
+      nl[i] = neg_lse2[r0 + ty + R / 4 * i];
+      nd[i] = neg_delta[r0 + ty + R / 4 * i];
     }
   }
-  if (keys) {
-    store_rows<D, RI>(static_cast<float*>(a.dk) + offset(a.st[kDk], b, h, 0), a.st[kDk].n, r0, N, acc1, scale, ty, tx);
-    store_rows<D, RI>(static_cast<float*>(a.dv) + offset(a.st[kDv], b, h, 0), a.st[kDv].n, r0, N, acc2, 1.f, ty, tx);
-  } else {
-    store_rows<D, RI>(static_cast<float*>(a.dq) + offset(a.st[kDq], b, h, 0), a.st[kDq].n, r0, N, acc1, scale, ty, tx);
+  for (int buf = 0; more; buf ^= NB - 1) {
+    const int c0 = it.c0;
+    uint64_t set = ~0ull;           // per-token lists: the query tokens that keep the key block
+    if (a.masks) set = a.masks_t[(bh * a.nB + (keys ? mine : it.other)) * a.nB + (keys ? it.other : mine)];
+    if (keys) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        nl[j] = neg_lse2[c0 + tx + 16 * j];      // rows < Npad: the tables are padded
+        nd[j] = neg_delta[c0 + tx + 16 * j];
+      }
+    }
+    more = it.next();
+    if (NB == 2 && more) load(buf ^ 1, it.c0);
+    else loads_commit();
+    loads_wait<NB - 1>();
+    __syncthreads();
+    const float *c1 = cs + buf * 2 * PIECE, *c2 = c1 + PIECE;
+    float p[4][4], g[4][4];
+    dots<D, R>(p, r1, c1, ty, tx, kz);
+    dots<D, R>(g, r2, c2, ty, tx, kz);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i / (4 / KS) != kz) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = ty + R / 4 * i, col = tx + 16 * j, l = keys ? j : i;
+        const int qn = keys ? c0 + col : r0 + row, kn = keys ? r0 + row : c0 + col;
+        const bool on = kn < N && ((set >> (qn & 63)) & 1ull);
+        const float pr = on ? exp2f(fmaf(p[i][j], scale2, nl[l])) : 0.f;
+        sp[row * kPitch + col] = pr;
+        sd[row * kPitch + col] = on ? pr * (g[i][j] + nd[l]) : 0.f;
+      }
+    }
+    __syncthreads();
+    weighted<D, R>(acc1, sd, c1, ty, tx, kz);
+    if (keys) weighted<D, R>(acc2, sp, c2, ty, tx, kz);
+    __syncthreads();                // the piece's rows, P and dS may be overwritten
+    if (NB == 1 && more) load(0, it.c0);
   }
+  loads_wait<0>();
+  if (keys) {
+    store_rows<D, R>(static_cast<float*>(a.dk) + offset(a.st[kDk], b, h, 0), a.st[kDk].n, r0, N, acc1, scale, ty, tx, kz);
+    store_rows<D, R>(static_cast<float*>(a.dv) + offset(a.st[kDv], b, h, 0), a.st[kDv].n, r0, N, acc2, 1.f, ty, tx, kz);
+  } else {
+    store_rows<D, R>(static_cast<float*>(a.dq) + offset(a.st[kDq], b, h, 0), a.st[kDq].n, r0, N, acc1, scale, ty, tx, kz);
+  }
+}
+
+// blockIdx.x: tiles of keys (dk, dv), then tiles of queries (dq).
+template <int D, int R>
+__global__ void __launch_bounds__(256) attend_grad_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
+                                                             const float* __restrict__ v, const float* __restrict__ dout,
+                                                             const __grid_constant__ AttendGradArgs a, int tiles) {
+  extern __shared__ __align__(16) float sm[];
+  if (static_cast<int>(blockIdx.x) < tiles) f32_tile<D, R, true>(sm, q, k, v, dout, a, blockIdx.x);
+  else f32_tile<D, R, false>(sm, q, k, v, dout, a, blockIdx.x - tiles);
 }
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
