@@ -129,8 +129,11 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
 // by shuffles), then, P and dS in shared memory, 4 rows x d / 16 columns of the
 // sums over its share of the piece's rows.
 // Bound by shared-memory reads: 4 x 4 results a thread take 8 vectors for 64
-// FMAs, twice the reads that FMA issue would cover.  R = 64 wherever that fills
-// the SMs; with fewer rows R = 32 or 16 spreads them over more CTAs.
+// FMAs, twice the reads that FMA issue would cover (2,600 tokens, 4 heads of
+// 128, half of the blocks: 0.86 ms, 27 TFLOP/s of the seven products).  R = 64
+// wherever that fills the SMs; with fewer rows R = 32 or 16 spreads them over
+// more CTAs.  R = 64 / 32 / 16: 41 / 29 / 25 us for 256 tokens, 2 heads of 64
+// (16 CTAs with R = 64), 216 / 181 / 215 us for 1,000 tokens, 3 heads of 128 (96).
 constexpr int kPitch = 68;        // floats a row of P and dS: 16-byte rows, no bank conflicts
 
 // Rows r0 .. of a tensor into shared memory, zeros past N; cp.async, not waited for.

@@ -19,7 +19,9 @@
 // token tiles of one unit (up to kMaxHeads heads of one tensor and batch
 // element): a token's position, perm entry and (cos, sin) are looked up once
 // for its heads, the weight once for the block, and the next rows' loads are in
-// flight while a batch of rows is worked on.
+// flight while a batch of rows is worked on.  Rotation alone runs at the copy
+// rate (q and k of 32,760 tokens, 12 heads of 128: 403 MB in 62 us); with the
+// norm's row sums 604 MB take 104 us, 89 % of it.
 #include "lbsa_train_device.cuh"
 
 namespace lbsa {
@@ -268,10 +270,10 @@ __device__ __forceinline__ void async_16(uint32_t dst, const void* src, bool on)
 
 // Same tiling; x is read in source order, dy in block order, dx written in
 // source order.  A thread's rows come through its own slots of shared memory,
-// kStages - 1 batches ahead (no thread reads another's slots): with the next
-// batch in registers instead the kernel held 126 of them and took 168 us for a
-// layer's q, k, v (21 x 30 x 52 tokens, 12 heads of 128, bf16) where memory
-// needs 123.  A thread adds its columns' du n over all its rows; the block adds
+// kStages - 1 batches ahead (no thread reads another's slots).  For a layer's
+// q, k, v (21 x 30 x 52 tokens, 12 heads of 128, bf16), for which memory needs
+// 123 us, the call takes 151 us; with the next batch in registers instead the
+// kernel held 126 of them and the call took 168 us.  A thread adds its columns' du n over all its rows; the block adds
 // its groups' sums in a fixed order and writes one partial row, so the weight
 // gradient does not depend on the order in which blocks run.
 constexpr int kStages = 4;
@@ -458,8 +460,10 @@ __global__ void rope_table_kernel(RopePos p, double theta, double st, double sh,
 int token_tiles(int N, int d) { return (N + kThreads / (d / 8) - 1) / (kThreads / (d / 8)); }
 
 // Units: (batch, up to `heads` heads) of each item.  With few tokens the heads
-// are spread over more units, down to one head, until four blocks an SM have
-// work: a single token's 24 heads of 128 take 4 us so, 6 us as two units.
+// are spread over more units, down to one head, until every SM has a block: a
+// single token's 24 heads of 128 take 4.4 us so, 5.4 us as two units.  More
+// blocks than that cost more than they give: 924 tokens with 10 heads of 128,
+// half-split, take 6.7 us in 232 blocks and 11.4 us in 580.
 int plan_units(RopeArgs& a, const RopeItem* items, int count, int B, int N, int d, bool backward) {
   a.count = count;
   int total = 0;
@@ -476,13 +480,15 @@ int plan_units(RopeArgs& a, const RopeItem* items, int count, int B, int N, int 
       }
       a.chunk_end[i] = total;
     }
-    if (static_cast<long long>(total) * token_tiles(N, d) >= 148 * 4) break;
+    if (static_cast<long long>(total) * token_tiles(N, d) >= 148) break;
   }
   return total;
 }
 
-// Blocks along the tokens: about kBlocksPerSm an SM in all, so that a block
-// walks several tiles and the backward pass has few partial rows.
+// Blocks along the tokens: about kBlocksPerSm an SM in all (three waves of the
+// three that fit), so that a block walks several tiles and the backward pass
+// has few partial rows; 8 against 6 for a layer's q, k, v (norm_rope, 21 x 30 x
+// 52 tokens, 12 heads of 128): 104 and 107 us.
 constexpr int kBlocksPerSm = 9;
 int token_blocks(int N, int d, int units) {
   return std::max(1, std::min(token_tiles(N, d), (148 * kBlocksPerSm + units - 1) / units));
