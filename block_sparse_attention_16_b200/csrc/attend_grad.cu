@@ -65,20 +65,33 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
     const long long bh = blockIdx.x / W;
     for (int i = threadIdx.x; i < 32 * W; i += kPrepThreads) bm[i] = 0u;
     __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int r = warp; r < 32; r += kPrepThreads / 32) {
-      const int i = w * 32 + r;
-      if (i >= a.nB) break;
-      const long long row = bh * a.nB + i;
-      const int cnt = a.counts[row];
-      for (int t = lane; t < cnt; t += 32) {
-        const int j = a.cols[row * a.nB + t];
-        if (j < 0 || j >= a.nB) {
+    // four rows a warp, their lists' loads in flight together
+    constexpr int ROWS = 32 / (kPrepThreads / 32);
+    const int lane = threadIdx.x & 31, i0 = w * 32 + (threadIdx.x >> 5) * ROWS;
+    const long long row = bh * a.nB + i0;
+    int cnt[ROWS], most = 0;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      cnt[r] = i0 + r < a.nB ? a.counts[row + r] : 0;
+      most = max(most, cnt[r]);
+    }
+    for (int t = lane; t < most; t += 32) {
+      int j[ROWS];
+      uint64_t set[ROWS];
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        j[r] = t < cnt[r] ? a.cols[(row + r) * a.nB + t] : 0;
+        set[r] = a.masks && t < cnt[r] ? a.masks[(row + r) * a.nB + t] : 0ull;
+      }
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        if (t >= cnt[r]) continue;
+        if (j[r] < 0 || j[r] >= a.nB) {
           raise_status(a.status, LBSA_ERR_BAD_INDEX);
           continue;
         }
-        atomicOr(&bm[r * W + (j >> 5)], 1u << (j & 31));
-        if (a.masks) a.masks_t[(bh * a.nB + j) * a.nB + i] = a.masks[row * a.nB + t];
+        atomicOr(&bm[(i0 + r - w * 32) * W + (j[r] >> 5)], 1u << (j[r] & 31));
+        if (a.masks) a.masks_t[(bh * a.nB + j[r]) * a.nB + i0 + r] = set[r];
       }
     }
     __syncthreads();

@@ -281,8 +281,10 @@ def test_streams_two_calls_at_once_and_captured_graphs(dtype):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             graphs.append((g, step()))
-    for g, _ in graphs:
-        g.replay()
+    for (g, _), s in zip(graphs, streams):                # at once, each with its own scratch
+        with torch.cuda.stream(s):
+            for _ in range(3):
+                g.replay()
     torch.cuda.synchronize()
     for got in both + [g for _, g in graphs]:
         for a, b in zip(got, want):
