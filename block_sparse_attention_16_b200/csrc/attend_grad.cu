@@ -283,7 +283,7 @@ __device__ __forceinline__ void f32_tile(float* sm, const float* q, const float*
                                          const AttendGradArgs& a, int tile) {
   constexpr int KS = 64 / R, NB = kF32Buffers<D, R>, PIECE = 64 * (D + 4);
   float *r1 = sm, *r2 = r1 + R * (D + 4), *cs = r2 + R * (D + 4), *sp = cs + NB * 2 * PIECE, *sd = sp + R * kPitch;
-  const int h = blockIdx.y, b = blockIdx.z;
+  const int h = blockIdx.y, b = keys ? blockIdx.z : blockIdx.z - a.B;
   const int kz = threadIdx.x % KS, tx = threadIdx.x / KS % 16, ty = threadIdx.x / (KS * 16);
   const int N = a.N_valid, shift = a.block == 128 ? 1 : 0, W = (a.nB + 31) >> 5;
   const long long bh = static_cast<long long>(b) * a.H + h;
@@ -367,14 +367,14 @@ __device__ __forceinline__ void f32_tile(float* sm, const float* q, const float*
   }
 }
 
-// blockIdx.x: tiles of keys (dk, dv), then tiles of queries (dq).
+// blockIdx.z: batch elements of keys (dk, dv), then of queries (dq): the shorter tiles fill the last wave.
 template <int D, int R>
 __global__ void __launch_bounds__(256) attend_grad_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
                                                              const float* __restrict__ v, const float* __restrict__ dout,
-                                                             const __grid_constant__ AttendGradArgs a, int tiles) {
+                                                             const __grid_constant__ AttendGradArgs a) {
   extern __shared__ __align__(16) float sm[];
-  if (static_cast<int>(blockIdx.x) < tiles) f32_tile<D, R, true>(sm, q, k, v, dout, a, blockIdx.x);
-  else f32_tile<D, R, false>(sm, q, k, v, dout, a, blockIdx.x - tiles);
+  if (static_cast<int>(blockIdx.z) < a.B) f32_tile<D, R, true>(sm, q, k, v, dout, a, blockIdx.x);
+  else f32_tile<D, R, false>(sm, q, k, v, dout, a, blockIdx.x);
 }
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -395,8 +395,7 @@ cudaError_t f32(const float* q, const float* k, const float* v, const float* dou
   cudaError_t e = cudaFuncSetAttribute(attend_grad_f32_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int tiles = (a.N_valid + R - 1) / R;
-  return launch_dependent(attend_grad_f32_kernel<D, R>, dim3(2 * tiles, a.H, a.B), dim3(256), smem, s, q, k, v, dout, a,
-                          tiles);
+  return launch_dependent(attend_grad_f32_kernel<D, R>, dim3(tiles, a.H, 2 * a.B), dim3(256), smem, s, q, k, v, dout, a);
 }
 
 template <int D>

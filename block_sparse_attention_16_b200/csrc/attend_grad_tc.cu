@@ -171,15 +171,13 @@ __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const C
                                         const AttendGradArgs& a, const Tile& t, Walk walk, uint32_t* entries,
                                         volatile int* abort_flag) {
   using L = Layout<D, KEYS>;
-  if (t.n_steps == 0) {
-    if (KEYS) mbar_wait(bars.r_full, 0, a.wait_limit, a.status, nullptr);      // the own rows land before the CTA exits
-    return;
-  }
   uint32_t e[2], ahead[2];          // entries of this step, of the next one
   int done1 = 0, done2 = 0, done_col = 0;
-  // step j's first operand into the stage that step j - 3 had, its entries into the slots that step j - 4 had
+  // step j's first operand into the stage that step j - 3 had, its entries into
+  // the slots that step j - 4 had; false past the last step
   auto first = [&](int j, int stage) {
     ahead[0] = walk.next();
+    if (ahead[0] == 0u) return false;
     ahead[1] = walk.next();
     if (ahead[1] == 0u) ahead[1] = ahead[0] & kPiece;       // an odd tail: the piece again, kept by nobody
     entries[(j & 3) * 2] = ahead[0];
@@ -199,10 +197,14 @@ __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const C
     mbar_arrive_expect_tx(bars.c1_full + stage, L::TILE);
     for (int p = 0; p < 2; ++p) load_rows<D>(smem + L::OFF_C1 + stage * L::TILE, c1, bars.c1_full + stage, p, ahead[p] & kPiece, t);
     done1 = j + 1;
+    return true;
   };
-  first(0, 0);
+  if (!first(0, 0)) {
+    if (KEYS) mbar_wait(bars.r_full, 0, a.wait_limit, a.status, nullptr);      // the own rows land before the CTA exits
+    return;
+  }
   int stage = 1;                    // of step j + 1
-  for (int j = 0; j < t.n_steps; ++j) {
+  for (int j = 0;; ++j) {
     e[0] = ahead[0];
     e[1] = ahead[1];
     if (j >= N2 && !mbar_wait(bars.c2_empty + (j & 1), ((j >> 1) & 1) ^ 1, a.wait_limit, a.status, abort_flag)) break;
@@ -223,7 +225,7 @@ __device__ __forceinline__ void produce(uint8_t* smem, const Bars& bars, const C
       }
       done_col = j + 1;
     }
-    if (j + 1 < t.n_steps) first(j + 1, stage);
+    if (!first(j + 1, stage)) break;
     if (++stage == N1) stage = 0;
   }
   if (*abort_flag) {
@@ -381,6 +383,18 @@ __device__ __forceinline__ void score_gradients(uint32_t (&g)[kCols], const uint
   }
 }
 
+// 0 in the columns that do not count.  ROWS: `on` is all or nothing (a query row
+// keeps a whole piece or none of it) unless the piece is ragged.
+template <bool ROWS>
+__device__ __forceinline__ void keep_columns(uint32_t (&r)[kCols], uint32_t on, uint32_t whole) {
+  if (ROWS && whole) {
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) r[c] &= on;
+  } else {
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) r[c] = ((on >> c) & 1u) ? r[c] : 0u;
+  }
+}
 // rounded to bf16, two a column
 __device__ __forceinline__ void store_packed(uint32_t taddr, const uint32_t (&r)[kCols]) {
   uint32_t pk[kCols / 2];
@@ -465,8 +479,7 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
     if (!KEYS) warp_arrive(bars.s_done, lane);                       // the S columns are free
     probabilities<KEYS>(r, col, neg_lse, scale_log2);
     if (!all) {
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) r[c] = ((on >> c) & 1u) ? r[c] : 0u;
+      keep_columns<MASKED && !KEYS>(r, on, e & kWhole);
     }
     if (KEYS) {
       store_packed(s_col + buf * BN, r);
@@ -480,8 +493,7 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
     score_gradients<KEYS>(g, r, col + BN, neg_delta);
     if (!all) {
       // a pair that is not kept gets 0, whatever its dP holds
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) g[c] = ((on >> c) & 1u) ? g[c] : 0u;
+      keep_columns<MASKED && !KEYS>(g, on, e & kWhole);
     }
     store_packed(dp_col, g);
     warp_arrive(bars.ds_full, lane);
@@ -550,7 +562,8 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
   Tile t;
   t.tile = tile;
   t.h = blockIdx.y;
-  t.b = blockIdx.z;
+  t.b = KEYS ? blockIdx.z : blockIdx.z - a.B;
+  t.n_steps = 0;
   t.bh = static_cast<long long>(t.b) * a.H + t.h;
   // the tile's own rows do not depend on the tables: they are on their way while
   // the tables are waited for and the lists counted
@@ -572,25 +585,25 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
   const int first = shift ? tile : 2 * tile;
   const uint32_t* row0 = rows + (t.bh * a.nB + first) * W;
   const uint32_t* row1 = !shift && first + 1 < a.nB ? row0 + W : nullptr;
-  if (threadIdx.x < 128) {
-    int n = 0;
-    for (int w = threadIdx.x; w < W; w += 128) n += __popc(row0[w] | (row1 ? row1[w] : 0u));
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0 && n) atomicAdd(misc + 2, static_cast<uint32_t>(n));
-  }
-  __syncthreads();
-  t.n_steps = ((static_cast<int>(misc[2]) << shift) + 1) >> 1;
   if (warp == kProducer) {
+    // finds the end of the list itself: the first copies start while the others count
     if (lane == 0) {
       Walk walk;
       walk.init(row0, row1, W, shift, a.N_valid);
       if (KEYS) produce<D, KEYS, MASKED>(smem, bars, tq, tdo, a, t, walk, entries, abort_flag);
       else produce<D, KEYS, MASKED>(smem, bars, tk, tv, a, t, walk, entries, abort_flag);
     }
-  } else if (warp == kIssuer) {
-    issue<D, KEYS>(smem, bars, tmem, a, t.n_steps, abort_flag);
   } else {
-    softmax<D, KEYS, MASKED>(smem, bars, tmem, a, t, entries, scale_log2, scale, abort_flag);
+    if (threadIdx.x < 128) {
+      int n = 0;
+      for (int w = threadIdx.x; w < W; w += 128) n += __popc(row0[w] | (row1 ? row1[w] : 0u));
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0 && n) atomicAdd(misc + 2, static_cast<uint32_t>(n));
+    }
+    named_bar_sync(1, kThreads - 32);
+    t.n_steps = ((static_cast<int>(misc[2]) << shift) + 1) >> 1;
+    if (warp == kIssuer) issue<D, KEYS>(smem, bars, tmem, a, t.n_steps, abort_flag);
+    else softmax<D, KEYS, MASKED>(smem, bars, tmem, a, t, entries, scale_log2, scale, abort_flag);
   }
   tc_fence_before();
   __syncthreads();
@@ -604,12 +617,13 @@ template <int D, bool MASKED>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_grad_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
-                      const __grid_constant__ AttendGradArgs a, int tiles, float scale_log2, float scale) {
+                      const __grid_constant__ AttendGradArgs a, float scale_log2, float scale) {
   extern __shared__ __align__(1024) uint8_t smem[];
   // a CTA already gave up on a wait: skip the work, the call has failed
   if (*reinterpret_cast<volatile int32_t*>(a.status) == LBSA_ERR_TIMEOUT) return;
-  if (static_cast<int>(blockIdx.x) < tiles) run_tile<D, true, MASKED>(smem, &tq, &tk, &tv, &tdo, a, blockIdx.x, scale_log2, scale);
-  else run_tile<D, false, MASKED>(smem, &tq, &tk, &tv, &tdo, a, blockIdx.x - tiles, scale_log2, scale);
+  // keys first, all heads: the shorter tiles of the queries fill the last wave
+  if (static_cast<int>(blockIdx.z) < a.B) run_tile<D, true, MASKED>(smem, &tq, &tk, &tv, &tdo, a, blockIdx.x, scale_log2, scale);
+  else run_tile<D, false, MASKED>(smem, &tq, &tk, &tv, &tdo, a, blockIdx.x, scale_log2, scale);
 }
 
 }  // namespace
@@ -621,7 +635,7 @@ cudaError_t launch_attend_grad_tc(const CUtensorMap* tq, const CUtensorMap* tk, 
   auto go = [&](auto kern, int smem) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(2 * tiles, a.H, a.B), dim3(kThreads), smem, s, *tq, *tk, *tv, *tdo, a, tiles,
+    return launch_dependent(kern, dim3(tiles, a.H, 2 * a.B), dim3(kThreads), smem, s, *tq, *tk, *tv, *tdo, a,
                             static_cast<float>(1.4426950408889634 * scale), static_cast<float>(scale));
   };
   if (a.d == 128)

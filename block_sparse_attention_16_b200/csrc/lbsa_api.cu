@@ -691,7 +691,7 @@ int lbsa_attend_backward(const void* q, const void* k, const void* v, const void
   if (bs->B != desc->B || bs->H != desc->H || bs->nB != n_blocks(desc->N_valid, bs->block))
     return fail(LBSA_ERR_INVALID_ARG, "blockset (B=%d, H=%d, nB=%d, block=%d) does not match q (B=%d, H=%d, N=%d)",
                 bs->B, bs->H, bs->nB, bs->block, desc->B, desc->H, desc->N_valid);
-  if (desc->B > 65535 || desc->H > 65535) return fail(LBSA_ERR_UNSUPPORTED, "B or H exceeds 65535");
+  if (desc->B > 32767 || desc->H > 65535) return fail(LBSA_ERR_UNSUPPORTED, "B exceeds 32767 or H 65535");
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev != bs->device) return fail(LBSA_ERR_INVALID_ARG, "blockset lives on device %d, current is %d", bs->device, dev);

@@ -277,6 +277,7 @@ int lbsa_attend(const void* q, const void* k, const void* v, const lbsa_qkv_desc
  * bits.  Rows past N_valid are never read and never written.  A non-finite key
  * or value in a block that a row does not keep can reach that row when the
  * other 64-row half of its 128-row tile keeps the block, as in lbsa_attend.
+ * Limits: B <= 32767, H <= 65535 (LBSA_ERR_UNSUPPORTED beyond).
  * Scratch: 8 bytes a padded row, two bits a block pair, for per-token
  * blocksets 8 bytes a block pair, from the library pool. */
 int lbsa_attend_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
