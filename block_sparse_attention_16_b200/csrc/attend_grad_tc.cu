@@ -414,19 +414,19 @@ __device__ __forceinline__ void own_rows(const Bars& bars, uint32_t tmem, const 
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(wg & 1 ? a.dout : a.q) + t.b * st.b +
                                                     t.h * st.h + grow * st.n) + (wg >> 1) * (PART / 4);
   const uint32_t dst = tmem + (static_cast<uint32_t>(row & ~31) << 16) + (wg & 1 ? L::ROWS2 : L::ROWS1) + (wg >> 1) * PART;
+  uint32_t v[PART / 16][16];                     // every load in flight before the first store
 #pragma unroll
-  for (int c = 0; c < PART; c += 16) {
-    uint32_t v[16];
+  for (int c = 0; c < PART / 16; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 x = grow < a.N_valid ? __ldg(src + c / 4 + i) : make_uint4(0u, 0u, 0u, 0u);
-      v[4 * i] = x.x;
-      v[4 * i + 1] = x.y;
-      v[4 * i + 2] = x.z;
-      v[4 * i + 3] = x.w;
+      const uint4 x = grow < a.N_valid ? __ldg(src + c * 4 + i) : make_uint4(0u, 0u, 0u, 0u);
+      v[c][4 * i] = x.x;
+      v[c][4 * i + 1] = x.y;
+      v[c][4 * i + 2] = x.z;
+      v[c][4 * i + 3] = x.w;
     }
-    tmem_st16(dst + c, v);
-  }
+#pragma unroll
+  for (int c = 0; c < PART / 16; ++c) tmem_st16(dst + c * 16, v[c]);
   tmem_wait_st();
   warp_arrive(bars.r_full, threadIdx.x & 31);
 }
@@ -490,11 +490,7 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
     tc_fence_after();
     tmem_ld32(dp_col, g);
     tmem_wait_ld_dep(g);
-    score_gradients<KEYS>(g, r, col + BN, neg_delta);
-    if (!all) {
-      // a pair that is not kept gets 0, whatever its dP holds
-      keep_columns<MASKED && !KEYS>(g, on, e & kWhole);
-    }
+    score_gradients<KEYS>(g, r, col + BN, neg_delta);                // 0 where P is
     store_packed(dp_col, g);
     warp_arrive(bars.ds_full, lane);
   }

@@ -274,9 +274,10 @@ int lbsa_attend(const void* q, const void* k, const void* v, const lbsa_qkv_desc
  * nothing (lse = -inf) gives and gets no gradient; a key block that no query
  * keeps gets 0.  bf16: products on bf16 operands (P and dS rounded once), sums
  * in fp32.  The sums are taken in a fixed order: the same inputs give the same
- * bits.  Rows past N_valid are never read and never written.  A non-finite key
- * or value in a block that a row does not keep can reach that row when the
- * other 64-row half of its 128-row tile keeps the block, as in lbsa_attend.
+ * bits.  Rows past N_valid are never read and never written.  A non-finite
+ * element of a key block that a row does not keep can reach that row when
+ * another row of its 128-row tile keeps the block, as in lbsa_attend, and one
+ * of a query block a key block in the same way.
  * Limits: B <= 32767, H <= 65535 (LBSA_ERR_UNSUPPORTED beyond).
  * Scratch: 8 bytes a padded row, two bits a block pair, for per-token
  * blocksets 8 bytes a block pair, from the library pool. */
