@@ -433,8 +433,8 @@ __device__ __forceinline__ void own_rows(const Bars& bars, uint32_t tmem, const 
 
 template <int D, bool KEYS, bool MASKED>
 __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_t tmem, const AttendGradArgs& a,
-                                        const Tile& t, const uint32_t* entries, float scale_log2, float scale,
-                                        volatile int* abort_flag) {
+                                        const Tile& t, const uint32_t* entries, const CUtensorMap* out1,
+                                        const CUtensorMap* out2, float scale_log2, float scale, volatile int* abort_flag) {
   using L = Layout<D, KEYS>;
   const int lane = threadIdx.x & 31, wg = threadIdx.x >> 7, row = threadIdx.x & 127;
   const int half = row >> 6, grow = t.tile * BM + row;
@@ -500,40 +500,49 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
     sums = warp_wait(bars.drain, 0, wl, a.status, abort_flag);
     tc_fence_after();
   }
-  const bool valid = grow < a.N_valid;
-  auto store = [&](uint32_t acc, void* out, const GradStride& st, float f) {
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out) + t.b * st.b + t.h * st.h + grow * st.n;
-    for (int c = wg * 32; c < D; c += kGroups * 32) {
-      uint32_t o[32];
-      if (sums) {
-        tmem_ld32(t_lane + acc + c, o);
-        tmem_wait_ld_dep(o);
-      } else {
+  // Two warpgroups take a panel of 64 columns at a time: 32 columns a thread,
+  // rounded, into the first operand's ring (every product is done) in the
+  // swizzle of its tensor map, then one TMA store, which leaves out rows past
+  // N_valid.  (16-byte stores from the threads' rows took 5,200 cycles for dk and
+  // dv of d = 128.)
+  constexpr int PANELS = (KEYS ? 2 : 1) * (D / 64);
+  const int pr = wg >> 1;
+  for (int i = pr; i < PANELS; i += 2) {
+    const int acc = i / (D / 64), c64 = (i % (D / 64)) * 64;
+    const float f = KEYS && acc == 1 ? 1.f : scale;
+    uint32_t o[32];
+    if (sums) {
+      tmem_ld32(t_lane + (acc == 1 ? L::ACC2 : L::ACC1) + c64 + (wg & 1) * 32, o);
+      tmem_wait_ld_dep(o);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = 0u;
-      }
-      if (valid) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          reinterpret_cast<uint4*>(dst + c)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-      }
+      for (int j = 0; j < 32; ++j) o[j] = 0u;
     }
-  };
-  if (KEYS) {
-    store(L::ACC1, a.dk, a.st[kDk], scale);
-    store(L::ACC2, a.dv, a.st[kDv], 1.f);
-  } else {
-    store(L::ACC1, a.dq, a.st[kDq], scale);
+    uint8_t* panel = smem + L::OFF_C1 + i * BM * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t pk[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        pk[e] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * e]) * f, __uint_as_float(o[8 * j + 2 * e + 1]) * f);
+      *reinterpret_cast<uint4*>(panel + row * 128 + ((((wg & 1) * 4 + j) ^ (row & 7)) << 4)) =
+          make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    }
+    fence_proxy_async_smem();
+    named_bar_sync(2 + pr, 256);
+    if ((threadIdx.x & 255) == 0) {
+      tma_store_4d(acc == 1 ? out2 : out1, panel, c64, t.tile * BM, t.h, t.b);
+      tma_store_commit();
+    }
   }
+  if ((threadIdx.x & 255) == 0) tma_store_wait_read<0>();
 }
 
 template <int D, bool KEYS, bool MASKED>
 __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, const CUtensorMap* tk,
-                                         const CUtensorMap* tv, const CUtensorMap* tdo, const AttendGradArgs& a, int tile,
-                                         float scale_log2, float scale) {
+                                         const CUtensorMap* tv, const CUtensorMap* tdo, const CUtensorMap* out1,
+                                         const CUtensorMap* out2, const AttendGradArgs& a, int tile, float scale_log2,
+                                         float scale) {
   using L = Layout<D, KEYS>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Bars bars = make_bars(smem + L::OFF_BAR);
@@ -599,7 +608,7 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
     named_bar_sync(1, kThreads - 32);
     t.n_steps = ((static_cast<int>(misc[2]) << shift) + 1) >> 1;
     if (warp == kIssuer) issue<D, KEYS>(smem, bars, tmem, a, t.n_steps, abort_flag);
-    else softmax<D, KEYS, MASKED>(smem, bars, tmem, a, t, entries, scale_log2, scale, abort_flag);
+    else softmax<D, KEYS, MASKED>(smem, bars, tmem, a, t, entries, out1, out2, scale_log2, scale, abort_flag);
   }
   tc_fence_before();
   __syncthreads();
@@ -613,25 +622,26 @@ template <int D, bool MASKED>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_grad_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
-                      const __grid_constant__ AttendGradArgs a, float scale_log2, float scale) {
+                      const __grid_constant__ CUtensorMap tdq, const __grid_constant__ CUtensorMap tdk,
+                      const __grid_constant__ CUtensorMap tdv, const __grid_constant__ AttendGradArgs a, float scale_log2,
+                      float scale) {
   extern __shared__ __align__(1024) uint8_t smem[];
   // a CTA already gave up on a wait: skip the work, the call has failed
   if (*reinterpret_cast<volatile int32_t*>(a.status) == LBSA_ERR_TIMEOUT) return;
   // keys first, all heads: the shorter tiles of the queries fill the last wave
-  if (static_cast<int>(blockIdx.z) < a.B) run_tile<D, true, MASKED>(smem, &tq, &tk, &tv, &tdo, a, blockIdx.x, scale_log2, scale);
-  else run_tile<D, false, MASKED>(smem, &tq, &tk, &tv, &tdo, a, blockIdx.x, scale_log2, scale);
+  if (static_cast<int>(blockIdx.z) < a.B) run_tile<D, true, MASKED>(smem, &tq, &tk, &tv, &tdo, &tdk, &tdv, a, blockIdx.x, scale_log2, scale);
+  else run_tile<D, false, MASKED>(smem, &tq, &tk, &tv, &tdo, &tdq, nullptr, a, blockIdx.x, scale_log2, scale);
 }
 
 }  // namespace
 
-cudaError_t launch_attend_grad_tc(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
-                                  const CUtensorMap* tdo, const AttendGradArgs& a, cudaStream_t s) {
+cudaError_t launch_attend_grad_tc(const CUtensorMap* in, const CUtensorMap* out, const AttendGradArgs& a, cudaStream_t s) {
   const int tiles = (a.N_valid + BM - 1) / BM;
   const double scale = 1.0 / std::sqrt(static_cast<double>(a.d));
   auto go = [&](auto kern, int smem) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(tiles, a.H, 2 * a.B), dim3(kThreads), smem, s, *tq, *tk, *tv, *tdo, a,
+    return launch_dependent(kern, dim3(tiles, a.H, 2 * a.B), dim3(kThreads), smem, s, in[0], in[1], in[2], in[3], out[0], out[1], out[2], a,
                             static_cast<float>(1.4426950408889634 * scale), static_cast<float>(scale));
   };
   if (a.d == 128)

@@ -704,20 +704,21 @@ int lbsa_attend_backward(const void* q, const void* k, const void* v, const void
   if ((rc = device_state(&ds)) != LBSA_OK) return rc;
   if ((rc = scratch_alloc(ds, lbsa::attend_grad_workspace(&a, nullptr), s, &ws)) != LBSA_OK) return rc;
   lbsa::attend_grad_workspace(&a, ws.ptr);
-  CUtensorMap maps[4];
+  CUtensorMap maps[7];
   if (desc->dtype == LBSA_BF16) {
-    const int which[4] = {lbsa::kQ, lbsa::kK, lbsa::kV, lbsa::kDout};
-    for (int i = 0; i < 4; ++i) {
+    const int which[7] = {lbsa::kQ, lbsa::kK, lbsa::kV, lbsa::kDout, lbsa::kDq, lbsa::kDk, lbsa::kDv};
+    for (int i = 0; i < 7; ++i) {
       lbsa_qkv_desc one = *desc;
       one.stride_b = st[which[i]].b;
       one.stride_h = st[which[i]].h;
       one.stride_n = st[which[i]].n;
-      if ((rc = make_tmap(&maps[i], ins[which[i]], &one, 64)) != LBSA_OK) return rc;
+      const void* p = which[i] < 5 ? ins[which[i]] : outs[which[i] - 5];
+      if ((rc = make_tmap(&maps[i], p, &one, i < 4 ? 64 : 128)) != LBSA_OK) return rc;
     }
   }
   cudaError_t e = lbsa::launch_attend_grad_prep(out, dout, lse, desc->dtype, a, s);
   if (e == cudaSuccess)
-    e = desc->dtype == LBSA_BF16 ? lbsa::launch_attend_grad_tc(&maps[0], &maps[1], &maps[2], &maps[3], a, s)
+    e = desc->dtype == LBSA_BF16 ? lbsa::launch_attend_grad_tc(maps, maps + 4, a, s)
                                  : lbsa::launch_attend_grad_f32(static_cast<const float*>(q), static_cast<const float*>(k),
                                                                 static_cast<const float*>(v),
                                                                 static_cast<const float*>(dout), a, s);

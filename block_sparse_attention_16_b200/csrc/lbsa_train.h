@@ -43,7 +43,7 @@ struct AttendGradArgs {
   const uint64_t* masks;        // per-token scope, as AttendArgs::masks
   int32_t* status;
   const void *q, *dout;         // a query tile's own rows are read without a tensor map
-  void *dq, *dk, *dv;
+  void *dq, *dk, *dv;           // fp32; bf16 gradients leave through tensor maps
   GradStride st[kGradTensors];
   long long wait_limit;
   // the call's tables (attend_grad_workspace)
@@ -58,9 +58,9 @@ struct AttendGradArgs {
 size_t attend_grad_workspace(AttendGradArgs* a, void* base);
 cudaError_t launch_attend_grad_prep(const void* out, const void* dout, const float* lse, int dtype,
                                     const AttendGradArgs& a, cudaStream_t s);
-// bf16 on the tensor cores (attend_grad_tc.cu); the maps' boxes are 64 columns x 64 rows
-cudaError_t launch_attend_grad_tc(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
-                                  const CUtensorMap* tdo, const AttendGradArgs& a, cudaStream_t s);
+// bf16 on the tensor cores (attend_grad_tc.cu); in: q, k, v, dout with boxes of
+// 64 columns x 64 rows, out: dq, dk, dv with boxes of 64 x 128
+cudaError_t launch_attend_grad_tc(const CUtensorMap* in, const CUtensorMap* out, const AttendGradArgs& a, cudaStream_t s);
 cudaError_t launch_attend_grad_f32(const float* q, const float* k, const float* v, const float* dout,
                                    const AttendGradArgs& a, cudaStream_t s);
 
