@@ -136,17 +136,16 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
 
 // ------------------------------------------------------------------ CUDA cores
 // A CTA owns R rows (keys, or queries) and walks the 64-row pieces of the
-// other side that its block is kept with.  256 threads as R / 4 x 16 x 64 / R:
-// thread (ty, tx, kz) computes S and dP for rows ty + R / 4 i and columns
-// tx + 16 j over its share of the elements (the 64 / R threads of a share sum
-// by shuffles), then, P and dS in shared memory, 4 rows x d / 16 columns of the
-// sums over its share of the piece's rows.
-// Bound by shared-memory reads: 4 x 4 results a thread take 8 vectors for 64
-// FMAs, twice the reads that FMA issue would cover (2,600 tokens, 4 heads of
-// 128, half of the blocks: 0.86 ms, 27 TFLOP/s of the seven products).  R = 64
-// wherever that fills the SMs; with fewer rows R = 32 or 16 spreads them over
-// more CTAs.  R = 64 / 32 / 16: 41 / 29 / 25 us for 256 tokens, 2 heads of 64
-// (16 CTAs with R = 64), 216 / 181 / 215 us for 1,000 tokens, 3 heads of 128 (96).
+// other side that its block is kept with.  Two groups of 128 threads: the first
+// computes S and P, the second dP and dS; then the first adds to dv, the second
+// to dk (or, for dq, each over half of the piece's rows).  A group's threads
+// stand R / 8 x 16 x 64 / R: thread (ty, tx, kz) takes rows ty + R / 8 i and
+// columns tx + 16 j over its share of the elements (the 64 / R threads of a
+// share sum by shuffles).
+// Bound by shared-memory reads: 8 x 4 results take 12 vectors for 128 FMAs,
+// where FMA issue would cover 8 (4 x 4 results a thread of one group of 256 took
+// 8 for 64, and FILLME).  R = 64 wherever that
+// fills the SMs; with fewer rows R = 32 or 16 spreads them over more CTAs.
 constexpr int kPitch = 68;        // floats a row of P and dS: 16-byte rows, no bank conflicts
 
 // Rows r0 .. of a tensor into shared memory, zeros past N; cp.async, not waited for.
@@ -197,49 +196,49 @@ __device__ __forceinline__ float sum_shares(float v) {
   return v;
 }
 
-// acc[i][j] = row ty + R / 4 i of x  .  row tx + 16 j of y
+// acc[i][j] = row ty + R / 8 i of x  .  row tx + 16 j of y
 template <int D, int R>
-__device__ __forceinline__ void dots(float (&acc)[4][4], const float* x, const float* y, int ty, int tx, int kz) {
+__device__ __forceinline__ void dots(float (&acc)[8][4], const float* x, const float* y, int ty, int tx, int kz) {
   constexpr int KS = 64 / R;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
   for (int e = 4 * kz; e < D; e += 4 * KS) {
-    float4 xr[4], yr[4];
+    float4 yr[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      xr[i] = *reinterpret_cast<const float4*>(x + (ty + R / 4 * i) * (D + 4) + e);
-      yr[i] = *reinterpret_cast<const float4*>(y + (tx + 16 * i) * (D + 4) + e);
-    }
+    for (int j = 0; j < 4; ++j) yr[j] = *reinterpret_cast<const float4*>(y + (tx + 16 * j) * (D + 4) + e);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i) {
+      const float4 xr = *reinterpret_cast<const float4*>(x + (ty + R / 8 * i) * (D + 4) + e);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        acc[i][j] = fmaf(xr[i].x, yr[j].x, fmaf(xr[i].y, yr[j].y, fmaf(xr[i].z, yr[j].z, fmaf(xr[i].w, yr[j].w, acc[i][j]))));
+        acc[i][j] = fmaf(xr.x, yr[j].x, fmaf(xr.y, yr[j].y, fmaf(xr.z, yr[j].z, fmaf(xr.w, yr[j].w, acc[i][j]))));
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = sum_shares<KS>(acc[i][j]);
 }
 
-// acc[i][.] += sum of w[ty + R / 4 i][c] y[c][columns of tx] over the thread's share of the c
+// acc[i][.] += sum of w[ty + R / 8 i][c] y[c][columns of tx] over the thread's share of c0 <= c < c1
 template <int D, int R>
-__device__ __forceinline__ void weighted(float (&acc)[4][D / 16], const float* w, const float* y, int ty, int tx, int kz) {
-#pragma unroll 2
-  for (int c = 4 * kz; c < 64; c += 4 * (64 / R)) {
-    float4 wr[4];
+__device__ __forceinline__ void weighted(float (&acc)[8][D / 16], const float* w, const float* y, int c0, int c1, int ty,
+                                         int tx, int kz) {
+#pragma unroll 1
+  for (int c = c0 + 4 * kz; c < c1; c += 4 * (64 / R)) {
+    float4 wr[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wr[i] = *reinterpret_cast<const float4*>(w + (ty + R / 4 * i) * kPitch + c);
+    for (int i = 0; i < 8; ++i) wr[i] = *reinterpret_cast<const float4*>(w + (ty + R / 8 * i) * kPitch + c);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
       for (int g = 0; g < D / 64; ++g) {
         const float4 v = *reinterpret_cast<const float4*>(y + (c + k) * (D + 4) + g * 64 + tx * 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const float p = k == 0 ? wr[i].x : k == 1 ? wr[i].y : k == 2 ? wr[i].z : wr[i].w;
           acc[i][g * 4 + 0] = fmaf(p, v.x, acc[i][g * 4 + 0]);
           acc[i][g * 4 + 1] = fmaf(p, v.y, acc[i][g * 4 + 1]);
@@ -251,22 +250,28 @@ __device__ __forceinline__ void weighted(float (&acc)[4][D / 16], const float* w
   }
 }
 
-// the shares' sums; each of a share's threads stores some of the rows
+// The shares' sums, plus the other group's where `more` holds them; each of a
+// share's threads stores some of the rows.
 template <int D, int R>
-__device__ __forceinline__ void store_rows(float* g, long long stride, int r0, int N, const float (&acc)[4][D / 16], float f,
-                                           int ty, int tx, int kz) {
+__device__ __forceinline__ void store_rows(float* g, long long stride, int r0, int N, const float (&acc)[8][D / 16], float f,
+                                           const float* more, int ty, int tx, int kz) {
   constexpr int KS = 64 / R;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + ty + R / 4 * i;
+  for (int i = 0; i < 8; ++i) {
+    const int row = ty + R / 8 * i, r = r0 + row;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       float4 v;
-      v.x = sum_shares<KS>(acc[i][c * 4]) * f;
-      v.y = sum_shares<KS>(acc[i][c * 4 + 1]) * f;
-      v.z = sum_shares<KS>(acc[i][c * 4 + 2]) * f;
-      v.w = sum_shares<KS>(acc[i][c * 4 + 3]) * f;
-      if (r < N && i / (4 / KS) == kz) *reinterpret_cast<float4*>(g + r * stride + c * 64 + tx * 4) = v;
+      v.x = sum_shares<KS>(acc[i][c * 4]);
+      v.y = sum_shares<KS>(acc[i][c * 4 + 1]);
+      v.z = sum_shares<KS>(acc[i][c * 4 + 2]);
+      v.w = sum_shares<KS>(acc[i][c * 4 + 3]);
+      if (more) {
+        const float4 m = *reinterpret_cast<const float4*>(more + row * (D + 4) + c * 64 + tx * 4);
+        v = make_float4(v.x + m.x, v.y + m.y, v.z + m.z, v.w + m.w);
+      }
+      if (r < N && i / (8 / KS) == kz)
+        *reinterpret_cast<float4*>(g + r * stride + c * 64 + tx * 4) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
     }
   }
 }
@@ -284,24 +289,23 @@ __device__ __forceinline__ void f32_tile(float* sm, const float* q, const float*
   constexpr int KS = 64 / R, NB = kF32Buffers<D, R>, PIECE = 64 * (D + 4);
   float *r1 = sm, *r2 = r1 + R * (D + 4), *cs = r2 + R * (D + 4), *sp = cs + NB * 2 * PIECE, *sd = sp + R * kPitch;
   const int h = blockIdx.y, b = keys ? blockIdx.z : blockIdx.z - a.B;
-  const int kz = threadIdx.x % KS, tx = threadIdx.x / KS % 16, ty = threadIdx.x / (KS * 16);
+  const int group = threadIdx.x >> 7, lane = threadIdx.x & 127;
+  const int kz = lane % KS, tx = lane / KS % 16, ty = lane / (KS * 16);
   const int N = a.N_valid, shift = a.block == 128 ? 1 : 0, W = (a.nB + 31) >> 5;
   const long long bh = static_cast<long long>(b) * a.H + h;
   const GradStride &s_r1 = a.st[keys ? kK : kQ], &s_r2 = a.st[keys ? kV : kDout];
   const GradStride &s_c1 = a.st[keys ? kQ : kK], &s_c2 = a.st[keys ? kDout : kV];
   const float* g1 = (keys ? q : k) + offset(s_c1, b, h, 0);
   const float* g2 = (keys ? dout : v) + offset(s_c2, b, h, 0);
-  const float* neg_lse2 = a.neg_lse2 + bh * a.Npad;
-  const float* neg_delta = a.neg_delta + bh * a.Npad;
   const int r0 = tile * R, mine = r0 / a.block;
   const float scale = 1.0f / sqrtf(static_cast<float>(D)), scale2 = scale * kLog2e;
   load_rows<D>(r1, (keys ? k : q) + offset(s_r1, b, h, 0), s_r1.n, r0, R, N);
   load_rows<D>(r2, (keys ? v : dout) + offset(s_r2, b, h, 0), s_r2.n, r0, R, N);
-  float acc1[4][D / 16], acc2[4][D / 16];
+  float acc[8][D / 16];             // dv or dk by the group, or the group's share of dq
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) acc1[i][j] = acc2[i][j] = 0.f;
+    for (int j = 0; j < D / 16; ++j) acc[i][j] = 0.f;
   grid_wait();
   auto load = [&](int buf, int c0) {
     load_rows<D>(cs + buf * 2 * PIECE, g1, s_c1.n, c0, 64, N);
@@ -311,13 +315,11 @@ __device__ __forceinline__ void f32_tile(float* sm, const float* q, const float*
   Pieces it{(keys ? a.bits_t : a.bits) + (bh * a.nB + mine) * W, W, N, shift, -1, 0, 0u, 0, 0};
   bool more = it.next();
   if (more) load(0, it.c0);
-  float nl[4], nd[4];               // -lse, -D: of the thread's columns (keys) or rows (queries)
+  const float* column = (group ? a.neg_delta : a.neg_lse2) + bh * a.Npad;      // rows < Npad: the tables are padded
+  float nv[keys ? 4 : 8];           // -lse or -D of the thread's columns (keys) or rows (queries)
   if (!keys) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      nl[i] = neg_lse2[r0 + ty + R / 4 * i];
-      nd[i] = neg_delta[r0 + ty + R / 4 * i];
-    }
+    for (int i = 0; i < 8; ++i) nv[i] = column[r0 + ty + R / 8 * i];
   }
   for (int buf = 0; more; buf ^= NB - 1) {
     const int c0 = it.c0;
@@ -325,10 +327,7 @@ __device__ __forceinline__ void f32_tile(float* sm, const float* q, const float*
     if (a.masks) set = a.masks_t[(bh * a.nB + (keys ? mine : it.other)) * a.nB + (keys ? it.other : mine)];
     if (keys) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        nl[j] = neg_lse2[c0 + tx + 16 * j];      // rows < Npad: the tables are padded
-        nd[j] = neg_delta[c0 + tx + 16 * j];
-      }
+      for (int j = 0; j < 4; ++j) nv[j] = column[c0 + tx + 16 * j];
     }
     more = it.next();
     if (NB == 2 && more) load(buf ^ 1, it.c0);
@@ -336,34 +335,54 @@ __device__ __forceinline__ void f32_tile(float* sm, const float* q, const float*
     loads_wait<NB - 1>();
     __syncthreads();
     const float *c1 = cs + buf * 2 * PIECE, *c2 = c1 + PIECE;
-    float p[4][4], g[4][4];
-    dots<D, R>(p, r1, c1, ty, tx, kz);
-    dots<D, R>(g, r2, c2, ty, tx, kz);
+    float p[8][4];
+    dots<D, R>(p, group ? r2 : r1, group ? c2 : c1, ty, tx, kz);
+    if (group == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i / (4 / KS) != kz) continue;
+      for (int i = 0; i < 8; ++i) {
+        if (i / (8 / KS) != kz) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = ty + R / 4 * i, col = tx + 16 * j, l = keys ? j : i;
-        const int qn = keys ? c0 + col : r0 + row, kn = keys ? r0 + row : c0 + col;
-        const bool on = kn < N && ((set >> (qn & 63)) & 1ull);
-        const float pr = on ? exp2f(fmaf(p[i][j], scale2, nl[l])) : 0.f;
-        sp[row * kPitch + col] = pr;
-        sd[row * kPitch + col] = on ? pr * (g[i][j] + nd[l]) : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          const int row = ty + R / 8 * i, col = tx + 16 * j;
+          const int qn = keys ? c0 + col : r0 + row, kn = keys ? r0 + row : c0 + col;
+          const bool on = kn < N && ((set >> (qn & 63)) & 1ull);
+          sp[row * kPitch + col] = on ? exp2f(fmaf(p[i][j], scale2, nv[keys ? j : i])) : 0.f;
+        }
       }
     }
     __syncthreads();
-    weighted<D, R>(acc1, sd, c1, ty, tx, kz);
-    if (keys) weighted<D, R>(acc2, sp, c2, ty, tx, kz);
+    if (group == 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i / (8 / KS) != kz) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = (ty + R / 8 * i) * kPitch + tx + 16 * j;
+          sd[at] = sp[at] * (p[i][j] + nv[keys ? j : i]);
+        }
+      }
+    }
+    if (keys) {
+      if (group == 1) named_bar_sync(1, 128);
+      weighted<D, R>(acc, group ? sd : sp, group ? c1 : c2, 0, 64, ty, tx, kz);
+    } else {
+      __syncthreads();
+      weighted<D, R>(acc, sd, c1, 32 * group, 32 * group + 32, ty, tx, kz);
+    }
     __syncthreads();                // the piece's rows, P and dS may be overwritten
     if (NB == 1 && more) load(0, it.c0);
   }
   loads_wait<0>();
   if (keys) {
-    store_rows<D, R>(static_cast<float*>(a.dk) + offset(a.st[kDk], b, h, 0), a.st[kDk].n, r0, N, acc1, scale, ty, tx, kz);
-    store_rows<D, R>(static_cast<float*>(a.dv) + offset(a.st[kDv], b, h, 0), a.st[kDv].n, r0, N, acc2, 1.f, ty, tx, kz);
+    const GradStride& st = a.st[group ? kDk : kDv];
+    store_rows<D, R>(static_cast<float*>(group ? a.dk : a.dv) + offset(st, b, h, 0), st.n, r0, N, acc, group ? scale : 1.f,
+                     nullptr, ty, tx, kz);
   } else {
-    store_rows<D, R>(static_cast<float*>(a.dq) + offset(a.st[kDq], b, h, 0), a.st[kDq].n, r0, N, acc1, scale, ty, tx, kz);
+    // the second group's share through shared memory (the loop is over)
+    if (group == 1) store_rows<D, R>(cs, D + 4, 0, R, acc, 1.f, nullptr, ty, tx, kz);
+    __syncthreads();
+    if (group == 0)
+      store_rows<D, R>(static_cast<float*>(a.dq) + offset(a.st[kDq], b, h, 0), a.st[kDq].n, r0, N, acc, scale, cs, ty, tx, kz);
   }
 }
 
