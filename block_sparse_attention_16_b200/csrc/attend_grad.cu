@@ -143,9 +143,14 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
 // columns tx + 16 j over its share of the elements (the 64 / R threads of a
 // share sum by shuffles).
 // Bound by shared-memory reads: 8 x 4 results take 12 vectors for 128 FMAs,
-// where FMA issue would cover 8 (4 x 4 results a thread of one group of 256 took
-// 8 for 64, and FILLME).  R = 64 wherever that
-// fills the SMs; with fewer rows R = 32 or 16 spreads them over more CTAs.
+// where FMA issue would cover 8.  (With one group of 256 threads, 4 x 4 results
+// took 8 for 64: 2,600 tokens, 4 heads of 128, half of the blocks, 0.89 ms
+// against 0.82.)  24 such heads: 4.0 ms, 37 TFLOP/s of the seven products, half
+// of what the FMA pipes can do.
+// R = 64 wherever that fills the SMs; with fewer rows R = 32 or 16 spreads them
+// over more CTAs.  A call with R = 64 / 32 / 16: 41 / 31 / 27 us for 256 tokens,
+// 2 heads of 64 (16 CTAs with R = 64), 200 / 151 / 191 us for 1,000 tokens,
+// 3 heads of 128 (96), 277 / 333 / 518 us for 1,500 tokens, 8 heads of 64 (384).
 constexpr int kPitch = 68;        // floats a row of P and dS: 16-byte rows, no bank conflicts
 
 // Rows r0 .. of a tensor into shared memory, zeros past N; cp.async, not waited for.
