@@ -21,7 +21,7 @@
 // for its heads, the weight once for the block, and the next rows' loads are in
 // flight while a batch of rows is worked on.  Rotation alone runs at the copy
 // rate (q and k of 32,760 tokens, 12 heads of 128: 403 MB in 62 us); with the
-// norm's row sums 604 MB take 104 us, 89 % of it.
+// norm's row sums 604 MB take 96 us, 96 % of it.
 #include "lbsa_train_device.cuh"
 
 namespace lbsa {
@@ -186,22 +186,22 @@ __device__ __forceinline__ Unit unit_of(const RopeArgs& a, int y) {
   return u;
 }
 
-// grid (blocks along the tokens, units): a block takes kThreads / LANES tokens
-// at a time, token tiles blockIdx.x, blockIdx.x + gridDim.x, ... of one unit.
-template <typename T, int D, bool HALF>
-__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
+// What a unit's rows need is known to the compiler, so that a batch's rows are
+// worked on side by side, without a branch between them: for a layer's q, k, v
+// (21 x 30 x 52 tokens, 12 heads of 128, bf16) the call takes 99 us, 105 us
+// where the kernel asks row by row.  A weight row for each head is read again
+// for each row (117 us), as eight more registers a head would not fit.
+template <typename T, int D, bool HALF, bool NORM, bool ROTATE, bool PER_HEAD>
+__device__ __forceinline__ void rope_rows(const RopeArgs& a, const RopeItem& it, const Unit& u) {
   constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
   constexpr int kBatch = 8 / sizeof(T);          // heads of a token that a thread loads together: 64 bytes
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const Unit u = unit_of(a, blockIdx.y);
-  const RopeItem& it = a.it[u.item];
   const T* x = static_cast<const T*>(it.x) + u.b * it.xs[0] + u.h0 * it.xs[1] + lane * 8;
   T* y = static_cast<T*>(it.y) + u.b * it.ys[0] + u.h0 * it.ys[1] + lane * 8;
   const int64_t x_head = it.xs[1], y_head = it.ys[1];
-  const bool norm = it.weight != nullptr, rotate = it.rotate, per_head = norm && it.weight_heads > 1;
   Turn<HALF> turn;
   float w[8];
-  if (norm) load_weight(it, u.h0, lane, D, w);
+  if (NORM && !PER_HEAD) load_weight(it, 0, lane, D, w);
   const float sign = a.inverse ? -1.f : 1.f;
   const int tiles = (a.N + GROUPS - 1) / GROUPS, batches = (u.nh + kBatch - 1) / kBatch;
 
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
     const T* row = x + static_cast<long long>(a.inverse ? slot : tok) * it.xs[2] + h * x_head;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
+      v[i].zero();
       if (tok >= 0 && h + i < u.nh) v[i].load(row + i * x_head);
-      else v[i].zero();
     }
   };
   int slot = blockIdx.x * GROUPS + group, tok = token_of(a, slot, lane == 0);
@@ -219,14 +219,14 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int next_slot = slot + gridDim.x * GROUPS;
     const int next_tok = tile + gridDim.x < tiles ? token_of(a, next_slot, lane == 0) : -1;
-    if (rotate) turn.look(a.pos, lane, max(tok, 0), sign);
+    if (ROTATE) turn.look(a.pos, lane, max(tok, 0), sign);
     T* out = y + static_cast<long long>(a.inverse ? tok : slot) * it.ys[2];
     for (int b = 0; b < batches; ++b) {
       const bool last = b + 1 == batches;
       load(nxt, last ? next_slot : slot, last ? next_tok : tok, last ? 0 : (b + 1) * kBatch);
       // the batch's row sums first, so that their shuffles overlap
       float r[kBatch];
-      if (norm) {
+      if (NORM) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           float f[8];
@@ -242,17 +242,19 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int h = b * kBatch + i;
-        float f[8];
-        cur[i].get(f);
-        if (norm) {
-          if (per_head) load_weight(it, u.h0 + min(h, u.nh - 1), lane, D, w);
+        T* dst = out + h * y_head;
+        if (NORM || ROTATE) {
+          float f[8];
+          cur[i].get(f);
+          if (NORM) {
+            if (PER_HEAD) load_weight(it, u.h0 + min(h, u.nh - 1), lane, D, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = f[j] * r[i] * w[j];
-        }
-        if (rotate) turn.apply(f, a.pos, lane, LANES);
-        if (tok >= 0 && h < u.nh) {
-          if (norm || rotate) Eight<T>::store(out + h * y_head, f);
-          else cur[i].copy_to(out + h * y_head);
+            for (int j = 0; j < 8; ++j) f[j] = f[j] * r[i] * w[j];
+          }
+          if (ROTATE) turn.apply(f, a.pos, lane, LANES);
+          if (tok >= 0 && h < u.nh) Eight<T>::store(dst, f);
+        } else if (tok >= 0 && h < u.nh) {
+          cur[i].copy_to(dst);
         }
       }
 #pragma unroll
@@ -260,6 +262,24 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
     }
     slot = next_slot;
     tok = next_tok;
+  }
+}
+
+// grid (blocks along the tokens, units): a block takes kThreads / LANES tokens
+// at a time, token tiles blockIdx.x, blockIdx.x + gridDim.x, ... of one unit.
+template <typename T, int D, bool HALF>
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
+  const Unit u = unit_of(a, blockIdx.y);
+  const RopeItem& it = a.it[u.item];
+  if (it.weight && it.weight_heads > 1) {
+    if (it.rotate) rope_rows<T, D, HALF, true, true, true>(a, it, u);
+    else rope_rows<T, D, HALF, true, false, true>(a, it, u);
+  } else if (it.weight) {
+    if (it.rotate) rope_rows<T, D, HALF, true, true, false>(a, it, u);
+    else rope_rows<T, D, HALF, true, false, false>(a, it, u);
+  } else {
+    if (it.rotate) rope_rows<T, D, HALF, false, true, false>(a, it, u);
+    else rope_rows<T, D, HALF, false, false, false>(a, it, u);
   }
 }
 
@@ -272,33 +292,30 @@ __device__ __forceinline__ void async_16(uint32_t dst, const void* src, bool on)
 // source order.  A thread's rows come through its own slots of shared memory,
 // kStages - 1 batches ahead (no thread reads another's slots).  For a layer's
 // q, k, v (21 x 30 x 52 tokens, 12 heads of 128, bf16), for which memory needs
-// 123 us, the call takes 151 us; with the next batch in registers instead the
-// kernel held 126 of them and the call took 168 us.  A thread adds its columns' du n over all its rows; the block adds
-// its groups' sums in a fixed order and writes one partial row, so the weight
-// gradient does not depend on the order in which blocks run.
+// 123 us, the kernel takes 132 us and the call 139 us (151 us where the kernel
+// asks row by row what a unit needs; 168 us with the next batch in registers).
+// A thread adds its columns' du n over all its rows; the block adds its groups'
+// sums in a fixed order and writes one partial row, so the weight gradient does
+// not depend on the order in which blocks run.
 constexpr int kStages = 4;
 constexpr int kStageVecs = 4;                    // 16-byte slots of a thread in a stage: 64 bytes of x and dy
 constexpr int kBackwardSmem = kStages * kStageVecs * kThreads * 16 + kThreads * 8 * 4;
 
-template <typename T, int D, bool HALF>
-__global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const __grid_constant__ RopeArgs a) {
+template <typename T, int D, bool HALF, bool NORM, bool ROTATE>
+__device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, const RopeItem& it, const Unit& u) {
   constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
   constexpr int VECS = sizeof(T) / 2;            // slots of a row's eight elements
   constexpr int kBatch = kStageVecs / (2 * VECS);
-  extern __shared__ __align__(16) uint8_t smem[];
   uint4* slots = reinterpret_cast<uint4*>(smem) + threadIdx.x;       // [stage][vec][thread]
   float* sum = reinterpret_cast<float*>(smem + kStages * kStageVecs * kThreads * 16);   // [GROUPS][D]
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const Unit u = unit_of(a, blockIdx.y);
-  const RopeItem& it = a.it[u.item];
-  const bool norm = it.weight != nullptr, rotate = it.rotate;
   // without a norm x is not read (it may be NULL)
-  const T* x = norm ? static_cast<const T*>(it.x) + u.b * it.xs[0] + u.h0 * it.xs[1] + lane * 8 : nullptr;
+  const T* x = NORM ? static_cast<const T*>(it.x) + u.b * it.xs[0] + u.h0 * it.xs[1] + lane * 8 : nullptr;
   const T* dy = static_cast<const T*>(it.dy) + u.b * it.ds[0] + u.h0 * it.ds[1] + lane * 8;
   T* dx = static_cast<T*>(it.y) + u.b * it.ys[0] + u.h0 * it.ys[1] + lane * 8;
   Turn<HALF> turn;
   float w[8], acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (norm) load_weight(it, u.h0, lane, D, w);                 // a weight row for each head: one head a unit
+  if (NORM) load_weight(it, u.h0, lane, D, w);                 // a weight row for each head: one head a unit
   const int tiles = (a.N + GROUPS - 1) / GROUPS, batches = (u.nh + kBatch - 1) / kBatch;
   const int stride = gridDim.x;
 
@@ -311,11 +328,11 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
     for (int i = 0; i < kBatch; ++i) {
       const bool on = f_tok >= 0 && f_h + i < u.nh;
       const T* rd = dy + (on ? f_slot * it.ds[2] + (f_h + i) * it.ds[1] : 0);
-      const T* rx = norm ? x + (on ? f_tok * it.xs[2] + (f_h + i) * it.xs[1] : 0) : rd;
+      const T* rx = NORM ? x + (on ? f_tok * it.xs[2] + (f_h + i) * it.xs[1] : 0) : rd;
 #pragma unroll
       for (int v = 0; v < VECS; ++v) {
         async_16(dst + (i * 2 * VECS + v) * kThreads * 16, reinterpret_cast<const uint4*>(rd) + v, on);
-        if (norm) async_16(dst + (i * 2 * VECS + VECS + v) * kThreads * 16, reinterpret_cast<const uint4*>(rx) + v, on);
+        if (NORM) async_16(dst + (i * 2 * VECS + VECS + v) * kThreads * 16, reinterpret_cast<const uint4*>(rx) + v, on);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
   int slot = blockIdx.x * GROUPS + group, tok = token_of(a, slot, false), stage = 0;
   for (int tile = blockIdx.x; tile < tiles; tile += stride) {
     const int next_tok = tile + stride < tiles ? token_of(a, slot + stride * GROUPS, lane == 0) : -1;
-    if (rotate) turn.look(a.pos, lane, max(tok, 0), -1.f);
+    if (ROTATE) turn.look(a.pos, lane, max(tok, 0), -1.f);
     T* out = dx + static_cast<long long>(tok) * it.ys[2];
     for (int b = 0; b < batches; ++b) {
       fetch();
@@ -351,9 +368,9 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
       for (int i = 0; i < kBatch; ++i) {
         take(cd[i], stage, i * 2 * VECS);
         cd[i].get(g[i]);
-        if (rotate) turn.apply(g[i], a.pos, lane, LANES);
+        if (ROTATE) turn.apply(g[i], a.pos, lane, LANES);
       }
-      if (norm) {
+      if (NORM) {
         // sum x^2 and sum dn x of the batch together: mean(dn n) = r mean(dn x)
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -373,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int h = b * kBatch + i;
-        if (norm) {
+        if (NORM) {
           Eight<T> cx;
           float n[8];
           take(cx, stage, i * 2 * VECS + VECS);
@@ -387,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
           }
         }
         if (tok >= 0 && h < u.nh) {
-          if (norm || rotate) Eight<T>::store(out + h * it.ys[1], g[i]);
+          if (NORM || ROTATE) Eight<T>::store(out + h * it.ys[1], g[i]);
           else cd[i].copy_to(out + h * it.ys[1]);
         }
       }
@@ -398,14 +415,29 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   grid_launch_dependents();
-  if (!norm) return;
+  if constexpr (NORM) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) sum[group * D + lane * 8 + j] = acc[j];
-  __syncthreads();
-  for (int e = threadIdx.x; e < D; e += kThreads) {
-    float t = 0.f;
-    for (int g = 0; g < GROUPS; ++g) t += sum[g * D + e];
-    a.partial[(static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * D + e] = t;
+    for (int j = 0; j < 8; ++j) sum[group * D + lane * 8 + j] = acc[j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < D; e += kThreads) {
+      float t = 0.f;
+      for (int g = 0; g < GROUPS; ++g) t += sum[g * D + e];
+      a.partial[(static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * D + e] = t;
+    }
+  }
+}
+
+template <typename T, int D, bool HALF>
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const __grid_constant__ RopeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const Unit u = unit_of(a, blockIdx.y);
+  const RopeItem& it = a.it[u.item];
+  if (it.weight) {
+    if (it.rotate) backward_rows<T, D, HALF, true, true>(smem, a, it, u);
+    else backward_rows<T, D, HALF, true, false>(smem, a, it, u);
+  } else {
+    if (it.rotate) backward_rows<T, D, HALF, false, true>(smem, a, it, u);
+    else backward_rows<T, D, HALF, false, false>(smem, a, it, u);
   }
 }
 
@@ -488,7 +520,7 @@ int plan_units(RopeArgs& a, const RopeItem* items, int count, int B, int N, int 
 // Blocks along the tokens: about kBlocksPerSm an SM in all (three waves of the
 // three that fit), so that a block walks several tiles and the backward pass
 // has few partial rows; 8 against 6 for a layer's q, k, v (norm_rope, 21 x 30 x
-// 52 tokens, 12 heads of 128): 104 and 107 us.
+// 52 tokens, 12 heads of 128), when they were compared: 104 and 107 us.
 constexpr int kBlocksPerSm = 9;
 int token_blocks(int N, int d, int units) {
   return std::max(1, std::min(token_tiles(N, d), (148 * kBlocksPerSm + units - 1) / units));
