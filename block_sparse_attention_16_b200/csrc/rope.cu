@@ -395,7 +395,8 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
           float n[8];
           take(cx, stage, i * 2 * VECS + VECS);
           cx.get(n);
-          const float r = rsqrtf(sums[2 * i] * (1.f / D) + a.eps);
+          // a row that is not there adds nothing, with eps = 0 (1 / 0) too
+          const float r = tok >= 0 && h < u.nh ? rsqrtf(sums[2 * i] * (1.f / D) + a.eps) : 0.f;
           const float k = sums[2 * i + 1] * (1.f / D) * r * r;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {

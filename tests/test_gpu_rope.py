@@ -49,7 +49,7 @@ def _pair_size(x, angles, layout):
 
 
 def _within(got, ref, bound):
-    bad = np.abs(got - ref) > bound
+    bad = ~(np.abs(got - ref) <= bound)                      # a NaN is off, too
     assert not bad.any(), f"{bad.sum()} of {bad.size} off; worst {np.max(np.abs(got - ref) / np.maximum(bound, 1e-300)):.3g}x of its bound"
 
 
@@ -164,6 +164,23 @@ def test_norm_without_rotation_and_zero_rows():
     (dx,), (dw,) = lbsa.lbsa_norm_rope_backward([torch.ones_like(x)], [x], [w])
     assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
     assert not y[:, :, 4].any()
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradients_without_an_eps(dtype, per_head):
+    # odd heads and tokens: the last tile's and batch's rows that are not there have 1 / sqrt(0)
+    x, dy = _normal(1, 1, 3, 37, 128, dtype=dtype), _normal(2, 1, 3, 37, 128, dtype=dtype)
+    w = 1 + 0.2 * _normal(3, *((3, 128) if per_head else (128,)))
+    (dx,), (dw,) = lbsa.lbsa_norm_rope_backward([dy], [x], [w], eps=0.0)
+    x64, dy64, w64 = (host(t).astype(np.float64) for t in (x, dy, w))
+    rdx, rdw = oracle.norm_rope_grad(dy64, x64, w64, eps=0.0)
+    r = 1 / np.sqrt((x64 * x64).mean(-1, keepdims=True))
+    n, wr = x64 * r, (w64[:, None] if per_head else w64)
+    slack = 32 * E * r * (np.abs(dy64 * wr) + np.abs(n) * np.abs(dy64 * wr * n).mean(-1, keepdims=True))
+    _within(host(dx), rdx, HALF[dtype] * np.abs(rdx) + slack)
+    total = np.abs(dy64 * n).sum((0, 2) if per_head else (0, 1, 2))
+    _within(host(dw), rdw, (3 * 3 + 64) * E * total)          # at most three token tiles, three heads in a row
 
 
 def test_bad_perm_entries_skip_their_row_and_are_reported():
