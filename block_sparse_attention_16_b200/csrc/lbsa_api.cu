@@ -941,7 +941,7 @@ int lbsa_norm_rope_backward(const lbsa_rope_item* items, int32_t count, int32_t 
   DeviceState* ds = nullptr;
   Scratch ws;
   if ((rc = device_state(&ds)) != LBSA_OK) return rc;
-  if ((rc = scratch_alloc(ds, lbsa::norm_rope_backward_workspace_bytes(it, count, B, N, d), s, &ws)) != LBSA_OK)
+  if ((rc = scratch_alloc(ds, lbsa::norm_rope_backward_workspace_bytes(it, count, B, N, d, dtype), s, &ws)) != LBSA_OK)
     return rc;
   cudaError_t e = lbsa::launch_norm_rope_backward(it, count, B, N, d, dtype, p, perm, static_cast<float>(eps), ws.ptr,
                                                   ds->status, s);

@@ -25,7 +25,7 @@ struct RopePos {
 };
 cudaError_t launch_rope(const RopeItem* items, int count, int B, int N, int d, int dtype, const RopePos& pos,
                         const int32_t* perm, float eps, int inverse, int32_t* status, cudaStream_t s);
-size_t norm_rope_backward_workspace_bytes(const RopeItem* items, int count, int B, int N, int d);
+size_t norm_rope_backward_workspace_bytes(const RopeItem* items, int count, int B, int N, int d, int dtype);
 cudaError_t launch_norm_rope_backward(const RopeItem* items, int count, int B, int N, int d, int dtype,
                                       const RopePos& pos, const int32_t* perm, float eps, void* workspace,
                                       int32_t* status, cudaStream_t s);

@@ -41,7 +41,7 @@ struct RopeArgs {
   float eps;
   int inverse;                   // rotation by -angle, scatter
   int32_t* status;
-  float* partial;                // backward: [gridDim.y][gridDim.x][d] weight gradients of a block
+  float* partial;                // backward: [weight rows of a unit][gridDim.y][gridDim.x][d], a block's weight gradients
 };
 
 template <typename T>
@@ -299,13 +299,16 @@ __device__ __forceinline__ void async_16(uint32_t dst, const void* src, bool on)
 // not depend on the order in which blocks run.
 constexpr int kStages = 4;
 constexpr int kStageVecs = 4;                    // 16-byte slots of a thread in a stage: 64 bytes of x and dy
+// heads of a token that a thread works on together
+template <typename T>
+__host__ __device__ constexpr int batch_heads() { return kStageVecs * 16 / (2 * 8 * sizeof(T)); }
 constexpr int kBackwardSmem = kStages * kStageVecs * kThreads * 16 + kThreads * 8 * 4;
 
-template <typename T, int D, bool HALF, bool NORM, bool ROTATE>
+template <typename T, int D, bool HALF, bool NORM, bool ROTATE, bool PER_HEAD>
 __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, const RopeItem& it, const Unit& u) {
   constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
   constexpr int VECS = sizeof(T) / 2;            // slots of a row's eight elements
-  constexpr int kBatch = kStageVecs / (2 * VECS);
+  constexpr int kBatch = batch_heads<T>(), ROWS = PER_HEAD ? kBatch : 1;   // weight rows of the unit
   uint4* slots = reinterpret_cast<uint4*>(smem) + threadIdx.x;       // [stage][vec][thread]
   float* sum = reinterpret_cast<float*>(smem + kStages * kStageVecs * kThreads * 16);   // [GROUPS][D]
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
@@ -314,9 +317,12 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
   const T* dy = static_cast<const T*>(it.dy) + u.b * it.ds[0] + u.h0 * it.ds[1] + lane * 8;
   T* dx = static_cast<T*>(it.y) + u.b * it.ys[0] + u.h0 * it.ys[1] + lane * 8;
   Turn<HALF> turn;
-  float w[8], acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (NORM) load_weight(it, u.h0, lane, D, w);                 // a weight row for each head: one head a unit
-  const int tiles = (a.N + GROUPS - 1) / GROUPS, batches = (u.nh + kBatch - 1) / kBatch;
+  float w[ROWS][8], acc[ROWS][8] = {};
+  if (NORM) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) load_weight(it, PER_HEAD ? u.h0 + min(i, u.nh - 1) : 0, lane, D, w[i]);
+  }
+  const int tiles = (a.N + GROUPS - 1) / GROUPS, batches = PER_HEAD ? 1 : (u.nh + kBatch - 1) / kBatch;
   const int stride = gridDim.x;
 
   // the batch to be fetched next: its tile, slot, token and head
@@ -382,7 +388,7 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             sums[2 * i] = fmaf(n[j], n[j], sums[2 * i]);
-            sums[2 * i + 1] = fmaf(g[i][j] * w[j], n[j], sums[2 * i + 1]);
+            sums[2 * i + 1] = fmaf(g[i][j] * w[i % ROWS][j], n[j], sums[2 * i + 1]);
           }
         }
         row_sums<LANES>(sums);
@@ -400,8 +406,8 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
           const float k = sums[2 * i + 1] * (1.f / D) * r * r;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            acc[j] = fmaf(g[i][j], n[j] * r, acc[j]);          // rows that are not there are 0
-            g[i][j] = r * fmaf(-n[j], k, g[i][j] * w[j]);
+            acc[i % ROWS][j] = fmaf(g[i][j], n[j] * r, acc[i % ROWS][j]);   // rows that are not there are 0
+            g[i][j] = r * fmaf(-n[j], k, g[i][j] * w[i % ROWS][j]);
           }
         }
         if (tok >= 0 && h < u.nh) {
@@ -418,12 +424,16 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
   grid_launch_dependents();
   if constexpr (NORM) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[group * D + lane * 8 + j] = acc[j];
-    __syncthreads();
-    for (int e = threadIdx.x; e < D; e += kThreads) {
-      float t = 0.f;
-      for (int g = 0; g < GROUPS; ++g) t += sum[g * D + e];
-      a.partial[(static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * D + e] = t;
+    for (int i = 0; i < ROWS; ++i) {
+      if (i) __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[group * D + lane * 8 + j] = acc[i][j];
+      __syncthreads();
+      for (int e = threadIdx.x; e < D; e += kThreads) {
+        float t = 0.f;
+        for (int g = 0; g < GROUPS; ++g) t += sum[g * D + e];
+        a.partial[(static_cast<long long>(i * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * D + e] = t;
+      }
     }
   }
 }
@@ -433,12 +443,15 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
   extern __shared__ __align__(16) uint8_t smem[];
   const Unit u = unit_of(a, blockIdx.y);
   const RopeItem& it = a.it[u.item];
-  if (it.weight) {
-    if (it.rotate) backward_rows<T, D, HALF, true, true>(smem, a, it, u);
-    else backward_rows<T, D, HALF, true, false>(smem, a, it, u);
+  if (it.weight && it.weight_heads > 1) {
+    if (it.rotate) backward_rows<T, D, HALF, true, true, true>(smem, a, it, u);
+    else backward_rows<T, D, HALF, true, false, true>(smem, a, it, u);
+  } else if (it.weight) {
+    if (it.rotate) backward_rows<T, D, HALF, true, true, false>(smem, a, it, u);
+    else backward_rows<T, D, HALF, true, false, false>(smem, a, it, u);
   } else {
-    if (it.rotate) backward_rows<T, D, HALF, false, true>(smem, a, it, u);
-    else backward_rows<T, D, HALF, false, false>(smem, a, it, u);
+    if (it.rotate) backward_rows<T, D, HALF, false, true, false>(smem, a, it, u);
+    else backward_rows<T, D, HALF, false, false, false>(smem, a, it, u);
   }
 }
 
@@ -455,12 +468,15 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const __grid_constant
   const RopeItem& it = a.it[item];
   const int first = item ? a.chunk_end[item - 1] : 0;
   const bool shared = it.weight_heads == 1;
-  // the units' partial rows lie together: all of the item's, or (one head a unit) one run a batch element
+  // the units' partial rows lie together: all of the item's, or (a weight row
+  // for each head: plane row % heads) one run a batch element
   const long long run = shared ? static_cast<long long>(a.chunk_end[item] - first) * gx : gx;
+  const int heads = a.heads[item], chunks = (it.H + heads - 1) / heads;
   double t = 0.0;
   grid_wait();
   for (int b = 0; b < (shared ? 1 : B); ++b) {
-    const float* p = a.partial + static_cast<long long>(first + (shared ? 0 : b * it.H + row)) * gx * a.d + e;
+    const long long at = shared ? first : static_cast<long long>(row % heads) * a.chunk_end[2] + first + b * chunks + row / heads;
+    const float* p = a.partial + at * gx * a.d + e;
 #pragma unroll 8
     for (long long i = threadIdx.y; i < run; i += 32) t += p[i * a.d];
   }
@@ -492,12 +508,15 @@ __global__ void rope_table_kernel(RopePos p, double theta, double st, double sh,
 
 int token_tiles(int N, int d) { return (N + kThreads / (d / 8) - 1) / (kThreads / (d / 8)); }
 
-// Units: (batch, up to `heads` heads) of each item.  With few tokens the heads
+int unit_rows(int dtype) { return dtype == LBSA_BF16 ? batch_heads<__nv_bfloat16>() : batch_heads<float>(); }
+
+// Units: (batch, up to `heads` heads) of each item; with a weight row for each
+// head up to `rows` of them.  With few tokens the heads
 // are spread over more units, down to one head, until every SM has a block: a
 // single token's 24 heads of 128 take 4.4 us so, 5.4 us as two units.  More
 // blocks than that cost more than they give: 924 tokens with 10 heads of 128,
 // half-split, take 6.7 us in 232 blocks and 11.4 us in 580.
-int plan_units(RopeArgs& a, const RopeItem* items, int count, int B, int N, int d, bool backward) {
+int plan_units(RopeArgs& a, const RopeItem* items, int count, int B, int N, int d, int rows) {
   a.count = count;
   int total = 0;
   for (int most = kMaxHeads; most >= 1; most /= 2) {
@@ -505,8 +524,8 @@ int plan_units(RopeArgs& a, const RopeItem* items, int count, int B, int N, int 
     for (int i = 0; i < 3; ++i) {
       if (i < count) {
         a.it[i] = items[i];
-        const bool own_rows = backward && items[i].weight && items[i].weight_heads > 1;
-        a.heads[i] = own_rows ? 1 : std::min(items[i].H, most);
+        const bool per_head = items[i].weight && items[i].weight_heads > 1;
+        a.heads[i] = std::min(items[i].H, per_head ? std::min(rows, most) : most);
         total += B * ((items[i].H + a.heads[i] - 1) / a.heads[i]);
       } else {
         a.heads[i] = 1;
@@ -558,14 +577,14 @@ cudaError_t launch_rope(const RopeItem* items, int count, int B, int N, int d, i
   a.eps = eps;
   a.inverse = inverse;
   a.status = status;
-  const int units = plan_units(a, items, count, B, N, d, false);
+  const int units = plan_units(a, items, count, B, N, d, kMaxHeads);
   return launch<false>(a, dtype, dim3(token_blocks(N, d, units), units), s);
 }
 
-size_t norm_rope_backward_workspace_bytes(const RopeItem* items, int count, int B, int N, int d) {
+size_t norm_rope_backward_workspace_bytes(const RopeItem* items, int count, int B, int N, int d, int dtype) {
   RopeArgs a{};
-  const int units = plan_units(a, items, count, B, N, d, true);
-  return static_cast<size_t>(units) * token_blocks(N, d, units) * d * sizeof(float);
+  const int rows = unit_rows(dtype), units = plan_units(a, items, count, B, N, d, rows);
+  return static_cast<size_t>(rows) * units * token_blocks(N, d, units) * d * sizeof(float);
 }
 
 cudaError_t launch_norm_rope_backward(const RopeItem* items, int count, int B, int N, int d, int dtype,
@@ -579,7 +598,7 @@ cudaError_t launch_norm_rope_backward(const RopeItem* items, int count, int B, i
   a.eps = eps;
   a.status = status;
   a.partial = static_cast<float*>(workspace);
-  const int units = plan_units(a, items, count, B, N, d, true);
+  const int units = plan_units(a, items, count, B, N, d, unit_rows(dtype));
   const int gx = token_blocks(N, d, units);
   cudaError_t e = launch<true>(a, dtype, dim3(gx, units), s);
   int rows = 0;
