@@ -44,12 +44,36 @@ struct RopeArgs {
   float* partial;                // backward: [weight rows of a unit][gridDim.y][gridDim.x][d], a block's weight gradients
 };
 
-template <typename T>
+// The elements of a row that a lane holds.
+// interleaved: eight in a row, pairs 4 l .. 4 l + 3.
+// half-split: element e of the first half pairs with e + rd / 2, so a lane
+// holds four of each half, 4 l .. and rd / 2 + 4 l ..: its pairs are the same
+// ones, and no element comes from another lane: a layer's norm and rotation
+// (21 x 30 x 52 tokens, q, k, v of 12 heads of 128) 108 us, 130 us with eight
+// shuffles a row.  Past rd eight in a row.
+struct Place {
+  int at, gap;                   // the first four; from there to the second four
+  __device__ __forceinline__ Place(bool half, const RopePos& pos, int lane) {
+    const int rd = pos.dt + pos.dh + pos.dw;
+    const bool split = half && lane * 8 < rd;
+    at = split ? lane * 4 : lane * 8;
+    gap = split ? rd / 2 : 4;
+  }
+};
+
+template <typename T, bool HALF>
 struct Eight;
-template <>
-struct Eight<__nv_bfloat16> {
+template <bool HALF>
+struct Eight<__nv_bfloat16, HALF> {
   uint4 v;
-  __device__ __forceinline__ void load(const void* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int gap) {
+    if (HALF) {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p)), b = __ldg(reinterpret_cast<const uint2*>(p + gap));
+      v = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      v = __ldg(reinterpret_cast<const uint4*>(p));
+    }
+  }
   __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -59,46 +83,52 @@ struct Eight<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
-  __device__ __forceinline__ static void store(void* p, const float (&f)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                              pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  __device__ __forceinline__ void copy_to(__nv_bfloat16* p, int gap) const {
+    if (HALF) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
+      *reinterpret_cast<uint2*>(p + gap) = make_uint2(v.z, v.w);
+    } else {
+      *reinterpret_cast<uint4*>(p) = v;
+    }
   }
-  __device__ __forceinline__ void copy_to(void* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, int gap, const float (&f)[8]) {
+    Eight e;
+    e.v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    e.copy_to(p, gap);
+  }
 };
-template <>
-struct Eight<float> {
+template <bool HALF>
+struct Eight<float, HALF> {
   float4 a, b;
-  __device__ __forceinline__ void load(const void* p) {
+  __device__ __forceinline__ void load(const float* p, int gap) {
     a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    b = __ldg(reinterpret_cast<const float4*>(p + (HALF ? gap : 4)));
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
-  __device__ __forceinline__ static void store(void* p, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ __forceinline__ void copy_to(float* p, int gap) const {
+    *reinterpret_cast<float4*>(p) = a;
+    *reinterpret_cast<float4*>(p + (HALF ? gap : 4)) = b;
   }
-  __device__ __forceinline__ void copy_to(void* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
+  __device__ __forceinline__ static void store(float* p, int gap, const float (&f)[8]) {
+    Eight e;
+    e.a = make_float4(f[0], f[1], f[2], f[3]);
+    e.b = make_float4(f[4], f[5], f[6], f[7]);
+    e.copy_to(p, gap);
   }
 };
 
-// A lane's share of the rotation.
-// interleaved: pairs 4 l .. 4 l + 3 lie in the lane's own eight elements.
-// half-split: element e of the first half pairs with e + rd / 2, which a lane
-// rd / 16 further holds; both lanes look the pair's eight entries up.
+// A lane's share of the rotation: pairs 4 l .. 4 l + 3.
 template <bool HALF>
 struct Turn {
-  static constexpr int P = HALF ? 8 : 4;
-  float c[P], s[P];
-  // token: source (raster) index; tokens past the grid and pairs past rd / 2 keep their place
+  float c[4], s[4];
+  bool on[4];                    // tokens past the grid and pairs past rd / 2 keep their place
+  // token: source (raster) index
   __device__ __forceinline__ void look(const RopePos& pos, int lane, int token, float sign) {
     const int ht = pos.dt >> 1, hh = pos.dh >> 1, hw = pos.dw >> 1, half = ht + hh + hw;
-    const int first = HALF ? (lane * 8 < half ? lane * 8 : lane * 8 - half) : lane * 4;
     const bool in = token < pos.tokens;
     const uint32_t area = static_cast<uint32_t>(pos.Hg) * pos.Wg;
     const uint32_t tok = static_cast<uint32_t>(in ? token : 0);
@@ -108,34 +138,22 @@ struct Turn {
     const int row_h = pos.T * ht + static_cast<int>(h) * hh - ht;
     const int row_w = pos.T * ht + pos.Hg * hh + static_cast<int>(w) * hw - ht - hh;
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const int p = first + j;
+    for (int j = 0; j < 4; ++j) {
+      const int p = lane * 4 + j;
       float2 cs = make_float2(1.f, 0.f);
-      if (in && p < half) cs = __ldg(pos.table + (p + (p < ht ? row_t : p < ht + hh ? row_h : row_w)));
+      on[j] = in && p < half;
+      if (on[j]) cs = __ldg(pos.table + (p + (p < ht ? row_t : p < ht + hh ? row_h : row_w)));
       c[j] = cs.x;
       s[j] = cs.y * sign;
     }
   }
-  // every lane of the warp takes part (half-split exchanges elements)
-  __device__ __forceinline__ void apply(float (&f)[8], const RopePos& pos, int lane, int lanes) const {
-    if (!HALF) {
+  __device__ __forceinline__ void apply(float (&f)[8]) const {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = f[2 * j], b = f[2 * j + 1];
-        f[2 * j] = a * c[j & (P - 1)] - b * s[j & (P - 1)];
-        f[2 * j + 1] = a * s[j & (P - 1)] + b * c[j & (P - 1)];
-      }
-    } else {
-      const int hl = (pos.dt + pos.dh + pos.dw) >> 4;       // lanes of a half
-      const bool lo = lane < hl, rot = lane < 2 * hl;
-      const int other = rot ? (lo ? lane + hl : lane - hl) : lane;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float o = __shfl_sync(0xffffffffu, f[j], other, lanes);
-        const float cj = c[j & (P - 1)], sj = s[j & (P - 1)];
-        // lo: a c - b s;  hi: a s + b c with a the other lane's element
-        f[j] = rot ? (lo ? f[j] * cj - o * sj : o * sj + f[j] * cj) : f[j];
-      }
+    for (int j = 0; j < 4; ++j) {
+      float &a = f[HALF ? j : 2 * j], &b = f[HALF ? j + 4 : 2 * j + 1];
+      const float x = a * c[j] - b * s[j], y = a * s[j] + b * c[j];
+      a = on[j] ? x : a;         // not x: an infinity beside it would make it NaN
+      b = on[j] ? y : b;
     }
   }
 };
@@ -149,15 +167,16 @@ __device__ __forceinline__ void row_sums(float (&v)[n]) {
     for (int i = 0; i < n; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
-__device__ __forceinline__ void load_weight(const RopeItem& it, int head, int lane, int d, float (&w)[8]) {
-  const long long at = static_cast<long long>(it.weight_heads > 1 ? head : 0) * d + lane * 8;
+template <bool HALF>
+__device__ __forceinline__ void load_weight(const RopeItem& it, int head, Place l, int d, float (&w)[8]) {
+  const long long at = static_cast<long long>(it.weight_heads > 1 ? head : 0) * d + l.at;
   if (it.weight_dtype == LBSA_F32) {
-    Eight<float> v;
-    v.load(static_cast<const float*>(it.weight) + at);
+    Eight<float, HALF> v;
+    v.load(static_cast<const float*>(it.weight) + at, l.gap);
     v.get(w);
   } else {
-    Eight<__nv_bfloat16> v;
-    v.load(static_cast<const __nv_bfloat16*>(it.weight) + at);
+    Eight<__nv_bfloat16, HALF> v;
+    v.load(static_cast<const __nv_bfloat16*>(it.weight) + at, l.gap);
     v.get(w);
   }
 }
@@ -190,31 +209,32 @@ __device__ __forceinline__ Unit unit_of(const RopeArgs& a, int y) {
 // worked on side by side, without a branch between them: for a layer's q, k, v
 // (21 x 30 x 52 tokens, 12 heads of 128, bf16) the call takes 99 us, 105 us
 // where the kernel asks row by row.  A weight row for each head is read again
-// for each row (117 us), as eight more registers a head would not fit.
+// for each row (120 us), as eight more registers a head would not fit.
 template <typename T, int D, bool HALF, bool NORM, bool ROTATE, bool PER_HEAD>
 __device__ __forceinline__ void rope_rows(const RopeArgs& a, const RopeItem& it, const Unit& u) {
   constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
   constexpr int kBatch = 8 / sizeof(T);          // heads of a token that a thread loads together: 64 bytes
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const T* x = static_cast<const T*>(it.x) + u.b * it.xs[0] + u.h0 * it.xs[1] + lane * 8;
-  T* y = static_cast<T*>(it.y) + u.b * it.ys[0] + u.h0 * it.ys[1] + lane * 8;
+  const Place pl(HALF, a.pos, lane);
+  const T* x = static_cast<const T*>(it.x) + u.b * it.xs[0] + u.h0 * it.xs[1] + pl.at;
+  T* y = static_cast<T*>(it.y) + u.b * it.ys[0] + u.h0 * it.ys[1] + pl.at;
   const int64_t x_head = it.xs[1], y_head = it.ys[1];
   Turn<HALF> turn;
   float w[8];
-  if (NORM && !PER_HEAD) load_weight(it, 0, lane, D, w);
+  if (NORM && !PER_HEAD) load_weight<HALF>(it, 0, pl, D, w);
   const float sign = a.inverse ? -1.f : 1.f;
   const int tiles = (a.N + GROUPS - 1) / GROUPS, batches = (u.nh + kBatch - 1) / kBatch;
 
-  auto load = [&](Eight<T> (&v)[kBatch], int slot, int tok, int h) {
+  auto load = [&](Eight<T, HALF> (&v)[kBatch], int slot, int tok, int h) {
     const T* row = x + static_cast<long long>(a.inverse ? slot : tok) * it.xs[2] + h * x_head;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       v[i].zero();
-      if (tok >= 0 && h + i < u.nh) v[i].load(row + i * x_head);
+      if (tok >= 0 && h + i < u.nh) v[i].load(row + i * x_head, pl.gap);
     }
   };
   int slot = blockIdx.x * GROUPS + group, tok = token_of(a, slot, lane == 0);
-  Eight<T> cur[kBatch], nxt[kBatch];
+  Eight<T, HALF> cur[kBatch], nxt[kBatch];
   load(cur, slot, tok, 0);
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int next_slot = slot + gridDim.x * GROUPS;
@@ -247,14 +267,14 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, const RopeItem& it,
           float f[8];
           cur[i].get(f);
           if (NORM) {
-            if (PER_HEAD) load_weight(it, u.h0 + min(h, u.nh - 1), lane, D, w);
+            if (PER_HEAD) load_weight<HALF>(it, u.h0 + min(h, u.nh - 1), pl, D, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = f[j] * r[i] * w[j];
           }
-          if (ROTATE) turn.apply(f, a.pos, lane, LANES);
-          if (tok >= 0 && h < u.nh) Eight<T>::store(dst, f);
+          if (ROTATE) turn.apply(f);
+          if (tok >= 0 && h < u.nh) Eight<T, HALF>::store(dst, pl.gap, f);
         } else if (tok >= 0 && h < u.nh) {
-          cur[i].copy_to(dst);
+          cur[i].copy_to(dst, pl.gap);
         }
       }
 #pragma unroll
@@ -283,20 +303,29 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
   }
 }
 
-// 16 bytes from global to shared memory, zeros where !on.
+// A lane's elements of a row from global to its slots of shared memory (16
+// bytes each, kThreads slots apart), zeros where !on.
 __device__ __forceinline__ void async_16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void async_row(uint32_t dst, const T* src, int gap, bool on) {
+  async_16(dst, src, on);
+  if (sizeof(T) == 4) async_16(dst + kThreads * 16, src + gap, on);
 }
 
 // Same tiling; x is read in source order, dy in block order, dx written in
 // source order.  A thread's rows come through its own slots of shared memory,
-// kStages - 1 batches ahead (no thread reads another's slots).  For a layer's
-// q, k, v (21 x 30 x 52 tokens, 12 heads of 128, bf16), for which memory needs
-// 123 us, the kernel takes 132 us and the call 139 us (151 us where the kernel
-// asks row by row what a unit needs; 168 us with the next batch in registers).
+// kStages - 1 batches ahead (another's slots are read within a half-split row
+// only).  For a layer's q, k, v (21 x 30 x 52 tokens, 12 heads of 128, bf16), for
+// which memory needs 123 us, the kernel takes 133 us and the call 137-143 us
+// (151 us where the kernel asks row by row what a unit needs; 168 us with the
+// next batch in registers).  Half-split rows: 143 us (172 us with pairs that are
+// exchanged between lanes, 171 us with copies of 8 bytes).
 // A thread adds its columns' du n over all its rows; the block adds its groups'
 // sums in a fixed order and writes one partial row, so the weight gradient does
-// not depend on the order in which blocks run.
+// not depend on the order in which blocks run.  With a weight row for each head
+// a unit is one batch of heads, with a sum each: 200 us, 305 us with one head.
 constexpr int kStages = 4;
 constexpr int kStageVecs = 4;                    // 16-byte slots of a thread in a stage: 64 bytes of x and dy
 // heads of a token that a thread works on together
@@ -312,15 +341,21 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
   uint4* slots = reinterpret_cast<uint4*>(smem) + threadIdx.x;       // [stage][vec][thread]
   float* sum = reinterpret_cast<float*>(smem + kStages * kStageVecs * kThreads * 16);   // [GROUPS][D]
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const Place pl(HALF, a.pos, lane);
+  // Half-split bf16 rows are fetched 16 bytes a lane like the others and each
+  // lane takes its two times four elements from the row's slots: 8-byte copies
+  // of its own would be twice as many.
+  constexpr bool SHARED = HALF && sizeof(T) == 2;
+  const int from = SHARED ? lane * 8 : pl.at;
   // without a norm x is not read (it may be NULL)
-  const T* x = NORM ? static_cast<const T*>(it.x) + u.b * it.xs[0] + u.h0 * it.xs[1] + lane * 8 : nullptr;
-  const T* dy = static_cast<const T*>(it.dy) + u.b * it.ds[0] + u.h0 * it.ds[1] + lane * 8;
-  T* dx = static_cast<T*>(it.y) + u.b * it.ys[0] + u.h0 * it.ys[1] + lane * 8;
+  const T* x = NORM ? static_cast<const T*>(it.x) + u.b * it.xs[0] + u.h0 * it.xs[1] + from : nullptr;
+  const T* dy = static_cast<const T*>(it.dy) + u.b * it.ds[0] + u.h0 * it.ds[1] + from;
+  T* dx = static_cast<T*>(it.y) + u.b * it.ys[0] + u.h0 * it.ys[1] + pl.at;
   Turn<HALF> turn;
   float w[ROWS][8], acc[ROWS][8] = {};
   if (NORM) {
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) load_weight(it, PER_HEAD ? u.h0 + min(i, u.nh - 1) : 0, lane, D, w[i]);
+    for (int i = 0; i < ROWS; ++i) load_weight<HALF>(it, PER_HEAD ? u.h0 + min(i, u.nh - 1) : 0, pl, D, w[i]);
   }
   const int tiles = (a.N + GROUPS - 1) / GROUPS, batches = PER_HEAD ? 1 : (u.nh + kBatch - 1) / kBatch;
   const int stride = gridDim.x;
@@ -335,11 +370,8 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
       const bool on = f_tok >= 0 && f_h + i < u.nh;
       const T* rd = dy + (on ? f_slot * it.ds[2] + (f_h + i) * it.ds[1] : 0);
       const T* rx = NORM ? x + (on ? f_tok * it.xs[2] + (f_h + i) * it.xs[1] : 0) : rd;
-#pragma unroll
-      for (int v = 0; v < VECS; ++v) {
-        async_16(dst + (i * 2 * VECS + v) * kThreads * 16, reinterpret_cast<const uint4*>(rd) + v, on);
-        if (NORM) async_16(dst + (i * 2 * VECS + VECS + v) * kThreads * 16, reinterpret_cast<const uint4*>(rx) + v, on);
-      }
+      async_row(dst + i * 2 * VECS * kThreads * 16, rd, pl.gap, on);
+      if (NORM) async_row(dst + (i * 2 + 1) * VECS * kThreads * 16, rx, pl.gap, on);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (++f_stage == kStages) f_stage = 0;
@@ -352,10 +384,17 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
       f_next = f_tile + stride < tiles ? token_of(a, f_slot + stride * GROUPS, false) : -1;
     }
   };
-  auto take = [&](Eight<T>& v, int stage, int vec) {
+  auto take = [&](Eight<T, HALF>& v, int stage, int vec) {
     uint4* to = reinterpret_cast<uint4*>(&v);
+    const uint4* own = slots + (stage * kStageVecs + vec) * kThreads;
+    if (SHARED) {
+      const T* row = reinterpret_cast<const T*>(own - lane) + pl.at;
+      const uint2 lo = *reinterpret_cast<const uint2*>(row), hi = *reinterpret_cast<const uint2*>(row + pl.gap);
+      to[0] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) to[i] = slots[(stage * kStageVecs + vec + i) * kThreads];
+      for (int i = 0; i < VECS; ++i) to[i] = own[i * kThreads];
+    }
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch();
@@ -366,21 +405,23 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
     if (ROTATE) turn.look(a.pos, lane, max(tok, 0), -1.f);
     T* out = dx + static_cast<long long>(tok) * it.ys[2];
     for (int b = 0; b < batches; ++b) {
+      if (SHARED) __syncwarp();                                // the slots refilled next are read by the row's lanes
       fetch();
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      Eight<T> cd[kBatch];
+      if (SHARED) __syncwarp();
+      Eight<T, HALF> cd[kBatch];
       float g[kBatch][8], sums[2 * kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         take(cd[i], stage, i * 2 * VECS);
         cd[i].get(g[i]);
-        if (ROTATE) turn.apply(g[i], a.pos, lane, LANES);
+        if (ROTATE) turn.apply(g[i]);
       }
       if (NORM) {
         // sum x^2 and sum dn x of the batch together: mean(dn n) = r mean(dn x)
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          Eight<T> cx;
+          Eight<T, HALF> cx;
           float n[8];
           take(cx, stage, i * 2 * VECS + VECS);
           cx.get(n);
@@ -397,7 +438,7 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
       for (int i = 0; i < kBatch; ++i) {
         const int h = b * kBatch + i;
         if (NORM) {
-          Eight<T> cx;
+          Eight<T, HALF> cx;
           float n[8];
           take(cx, stage, i * 2 * VECS + VECS);
           cx.get(n);
@@ -411,8 +452,8 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
           }
         }
         if (tok >= 0 && h < u.nh) {
-          if (NORM || ROTATE) Eight<T>::store(out + h * it.ys[1], g[i]);
-          else cd[i].copy_to(out + h * it.ys[1]);
+          if (NORM || ROTATE) Eight<T, HALF>::store(out + h * it.ys[1], pl.gap, g[i]);
+          else cd[i].copy_to(out + h * it.ys[1], pl.gap);
         }
       }
       if (++stage == kStages) stage = 0;
@@ -427,7 +468,7 @@ __device__ __forceinline__ void backward_rows(uint8_t* smem, const RopeArgs& a, 
     for (int i = 0; i < ROWS; ++i) {
       if (i) __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[group * D + lane * 8 + j] = acc[i][j];
+      for (int j = 0; j < 8; ++j) sum[group * D + pl.at + (j < 4 ? j : pl.gap + j - 4)] = acc[i][j];
       __syncthreads();
       for (int e = threadIdx.x; e < D; e += kThreads) {
         float t = 0.f;

@@ -166,6 +166,25 @@ def test_norm_without_rotation_and_zero_rows():
     assert not y[:, :, 4].any()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout,dims", [("interleaved", (6, 0, 4)), ("half", (16, 0, 16))])
+def test_what_keeps_its_place_is_copied(layout, dims, dtype):
+    # text tokens past the grid and elements past the rotated ones: infinities, NaN and -0 too
+    x = _normal(1, 1, 3, 29, 64, dtype=dtype)
+    rd = sum(dims)
+    odd = torch.tensor([float("inf"), 1.0, float("-inf"), float("nan"), -0.0, 2.0], device="cuda", dtype=dtype)
+    x[..., 24:, :] = odd.repeat(11)[:64]
+    x[..., rd:] = odd.repeat(10)[:64 - rd]
+    table = lbsa.lbsa_rope_table((2, 3, 4), dims)
+    for inverse in (False, True):
+        y, = lbsa.lbsa_rope([x], table, (2, 3, 4), dims, layout=layout, inverse=inverse)
+        assert torch.isfinite(y[..., :24, :rd]).all() and not torch.equal(y[..., :24, :rd], x[..., :24, :rd])
+        for got, want in ((y[..., 24:, :], x[..., 24:, :]), (y[..., rd:], x[..., rd:])):
+            assert torch.equal(got.isnan(), want.isnan())
+            assert torch.equal(got.nan_to_num(9.0, posinf=99.0, neginf=-99.0), want.nan_to_num(9.0, posinf=99.0, neginf=-99.0))
+            assert torch.equal(got.signbit() & ~want.isnan(), want.signbit() & ~want.isnan())
+
+
 @pytest.mark.parametrize("per_head", [False, True])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_gradients_without_an_eps(dtype, per_head):
