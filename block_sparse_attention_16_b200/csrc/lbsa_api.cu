@@ -270,6 +270,14 @@ int rope_items(const lbsa_rope_item* items, int count, int B, int N, int d, int 
         return fail(LBSA_ERR_INVALID_ARG, "weight has %d rows: 1 or H = %d wanted", a.weight_heads, a.H);
       if (backward && (rc = validate_ptr(a.dweight, "dweight")) != LBSA_OK) return rc;
     }
+    for (int j = 0; j < i; ++j) {
+      const lbsa_rope_item& o = items[j];
+      const bool reads_a = !backward || a.weight, reads_o = !backward || o.weight;
+      if (a.y == o.y || (reads_o && a.y == o.x) || (reads_a && o.y == a.x) || (backward && (a.y == o.dy || o.y == a.dy)))
+        return fail(LBSA_ERR_INVALID_ARG, "the output of one tensor may not alias another's input or output");
+      if (backward && a.weight && o.weight && a.dweight == o.dweight)
+        return fail(LBSA_ERR_INVALID_ARG, "two weights need a gradient buffer each");
+    }
     heads += static_cast<long long>(B) * a.H;
     lbsa::RopeItem& o = out[i];
     o = lbsa::RopeItem{a.x, a.y, a.dy, a.weight, a.dweight, a.H, pos && a.rotate, a.weight_dtype,

@@ -419,8 +419,9 @@ int lbsa_rope_table(const int32_t* grid, const int32_t* dims, double theta, cons
  *   inverse != 0:  y[perm[slot]] = R(perm[slot])^-1 x[slot]
  * (perm NULL: slot order is raster order).  The inverse undoes the call and is
  * its gradient.  perm as in lbsa_permute: an entry outside [0, N) skips its
- * row and records LBSA_ERR_BAD_INDEX in the per-device status word.  x and y
- * may not alias.  Products and sums in fp32, rounded once. */
+ * row and records LBSA_ERR_BAD_INDEX in the per-device status word.  No y may
+ * alias an input or another y of the call.  Products and sums in fp32, rounded
+ * once. */
 int lbsa_rope(const lbsa_rope_item* items, int32_t count, int32_t B, int32_t N, int32_t d, int32_t dtype,
               const lbsa_rope_pos* pos, const int32_t* perm, int32_t inverse, void* stream);
 
@@ -435,8 +436,10 @@ int lbsa_norm_rope(const lbsa_rope_item* items, int32_t count, int32_t B, int32_
 /* Its gradients: y[s] = dL/dx[s] and dweight = dL/dw from dy (block order) and
  * the same x (source order), weight, pos, perm and eps.  dweight is summed in
  * a fixed order (fp32 within a block of rows, 64 bits across blocks), so
- * repeated calls give the same bits.  Scratch: one fp32 row of d for each block
- * of the launch (about 1,200), from the library pool. */
+ * repeated calls give the same bits.  A weight that two tensors share has a
+ * dweight for each.  Scratch, from the library pool: one fp32 row of d (bf16
+ * tensors: two) for each block of the launch, of which there are about 1,300
+ * or, with more (batch, head) pairs than that, one for each. */
 int lbsa_norm_rope_backward(const lbsa_rope_item* items, int32_t count, int32_t B, int32_t N, int32_t d,
                             int32_t dtype, const lbsa_rope_pos* pos, const int32_t* perm, double eps, void* stream);
 

@@ -68,6 +68,19 @@ def test_sizes_are_checked(kw, code):
     assert _call("lbsa_rope", _item(weight=0), _pos(), last=0, **kw) == code
 
 
+@pytest.mark.parametrize("name,kw", [
+    ("lbsa_norm_rope", dict(y=2 * A)), ("lbsa_norm_rope", dict(y=A)), ("lbsa_norm_rope", dict(x=2 * A)),
+    ("lbsa_norm_rope_backward", dict(y=2 * A)), ("lbsa_norm_rope_backward", dict(y=A)),
+    ("lbsa_norm_rope_backward", dict(y=3 * A)), ("lbsa_norm_rope_backward", dict(x=2 * A)),
+    ("lbsa_norm_rope_backward", dict(dy=2 * A)), ("lbsa_norm_rope_backward", dict(dweight=5 * A)),
+])
+def test_tensors_of_one_call_do_not_alias(name, kw):
+    other = dict(x=11 * A, y=12 * A, dy=13 * A, weight=4 * A, dweight=15 * A)
+    items = (lbsa._RopeItem * 2)(_item(), _item(**{**other, **kw}))
+    rc = getattr(lbsa.load_library(), name)(items, 2, 1, 24, 64, 1, ctypes.byref(_pos()), None, 1e-6, None)
+    assert rc == INV and ("alias" in lbsa.lbsa_last_error() or "buffer each" in lbsa.lbsa_last_error())
+
+
 def test_eps_weight_and_missing_arguments():
     for eps in (-1e-6, float("nan"), float("inf")):
         assert _call("lbsa_norm_rope", _item(), _pos(), last=eps) == INV
