@@ -51,13 +51,13 @@ constexpr int kRowsPerBlock = 64;        // query rows of a block of the second 
 
 // Blocks [0, index_blocks): 32 query blocks of one (batch, head) each, whose
 // lists become bit rows and, transposed in shared memory, one word of every
-// key block's bits.  The others: 64 query rows each, D = dout . out.  Bound by
-// reading out and dout once.
+// key block's bits.  The others: 64 rows each, D = dout . out and, bf16, the sum
+// of the key rows.  Bound by reading out, dout and k once.
 template <typename T, int D>
 __global__ void __launch_bounds__(kPrepThreads)
 attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, const float* __restrict__ lse,
                         AttendGradArgs a, int index_blocks) {
-  extern __shared__ uint32_t bm[];                     // [32][W]
+  extern __shared__ uint32_t bm[];                     // [32][W], or the threads' key sums
   grid_launch_dependents();
   const int W = (a.nB + 31) >> 5;
   if (blockIdx.x < index_blocks) {
@@ -130,6 +130,31 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
       const bool none = l == -INFINITY;
       a.neg_lse2[row] = none ? -INFINITY : -l * kLog2e;
       a.neg_delta[row] = none ? 0.f : -sum;
+    }
+  }
+  if constexpr (sizeof(T) == 2) {
+    float* part = reinterpret_cast<float*>(bm);        // [GROUPS][D]
+    float s[8] = {};
+#pragma unroll
+    for (int i = 0; i < kRowsPerBlock / GROUPS; ++i) {
+      const int n = static_cast<int>(row0 + i * GROUPS + threadIdx.x / LANES - bh * a.Npad);
+      if (n >= a.N_valid) continue;
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + offset(a.st[kK], b, h, n)) + lane);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[2 * e] += __uint_as_float(w[e] << 16);
+        s[2 * e + 1] += __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[threadIdx.x / LANES * D + lane * 8 + e] = s[e];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float t = 0.f;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) t += part[g * D + threadIdx.x];
+      a.k_sums[row0 / kRowsPerBlock * D + threadIdx.x] = t;
     }
   }
 }
@@ -408,7 +433,9 @@ cudaError_t prep(const void* out, const void* dout, const float* lse, const Atte
   const long long W = (a.nB + 31) / 32, bh = static_cast<long long>(a.B) * a.H;
   const long long index_blocks = bh * W, row_blocks = bh * a.Npad / kRowsPerBlock;
   if (index_blocks + row_blocks > 2147483647ll) return cudaErrorInvalidValue;
-  attend_grad_prep_kernel<T, D><<<static_cast<unsigned>(index_blocks + row_blocks), kPrepThreads, 32 * W * 4, s>>>(
+  const size_t sums = sizeof(T) == 2 ? kPrepThreads * 8 * sizeof(float) : 0;
+  const size_t smem = std::max<size_t>(32 * W * 4, sums);
+  attend_grad_prep_kernel<T, D><<<static_cast<unsigned>(index_blocks + row_blocks), kPrepThreads, smem, s>>>(
       static_cast<const T*>(out), static_cast<const T*>(dout), lse, a, static_cast<int>(index_blocks));
   return cudaGetLastError();
 }
@@ -432,7 +459,7 @@ cudaError_t f32_rows(const float* q, const float* k, const float* v, const float
 
 }  // namespace
 
-size_t attend_grad_workspace(AttendGradArgs* a, void* base) {
+size_t attend_grad_workspace(AttendGradArgs* a, int dtype, void* base) {
   const size_t bh = static_cast<size_t>(a->B) * a->H, W = (a->nB + 31) / 32;
   a->Npad = (a->N_valid + 127) / 128 * 128;
   size_t at = 0;
@@ -441,13 +468,15 @@ size_t attend_grad_workspace(AttendGradArgs* a, void* base) {
     at += round256(bytes);
     return static_cast<char*>(base) + here;
   };
-  char* p[5];
+  char* p[6];
   p[0] = take(bh * a->Npad * sizeof(float));
   p[1] = take(bh * a->Npad * sizeof(float));
   p[2] = take(bh * a->nB * W * sizeof(uint32_t));
   p[3] = take(bh * a->nB * W * sizeof(uint32_t));
   p[4] = a->masks ? take(bh * a->nB * a->nB * sizeof(uint64_t)) : nullptr;
+  p[5] = dtype == LBSA_BF16 ? take(bh * (a->Npad / kRowsPerBlock) * a->d * sizeof(float)) : nullptr;
   if (base) {
+    a->k_sums = reinterpret_cast<float*>(p[5]);
     a->neg_lse2 = reinterpret_cast<float*>(p[0]);
     a->neg_delta = reinterpret_cast<float*>(p[1]);
     a->bits = reinterpret_cast<uint32_t*>(p[2]);

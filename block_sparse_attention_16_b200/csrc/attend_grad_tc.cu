@@ -28,15 +28,20 @@
 // whole bandwidth, and took 90 to 100 cycles.
 //
 // Roundings: P and dS become bf16 once, as operands (2^-9 relative); all else is
-// fp32.  D is taken from the rounded out.  dq is then 3.4e-3 off (Frobenius) where
-// rounding the exact result costs 1.7e-3: sum_c dS_rc = 0 cancels what the keys
-// have in common, the rounding errors do not.  dS as two bf16 terms would mend
-// that with an eighth product.
+// fp32.  D is taken from the rounded out.  sum_c dS_rc = 0 takes out of dq what
+// the keys have in common, but rounded dS sum to some e_r, which would bring it
+// back.  So dq_r = scale sum_c dS_rc (k_c - m), the same number for any m: m is
+// the mean of the tile's kept keys, and e_r m is taken off at the end.  Keys of
+// unit noise about a common vector of its size: dq 2.4e-3 off (Frobenius),
+// 3.4e-3 without m, where rounding the exact result costs 1.7e-3.  e_r adds a
+// mixed fp32 + bf16 addition an element, the rest little: 17.6 -> 17.9 ms below,
+// 0.1375 -> 0.1456 ms for 4,884 tokens, 128-token blocks, d = 64 (with the pairs
+// unpacked and added as fp32x2: 18.2 and 0.149 ms).
 //
 // What bounds it: 21 x 30 x 52 tokens, 12 heads of 128, 0.90 of the blocks kept
-// (0.97 of them in a tile's union): 15.9 ms from idle, 17.7 ms back to back, where
-// the card sits at its power limit (1.55 GHz); 839 TFLOP/s of the formula's
-// five products, 1,290 of the products done, 0.93 of what cuBLAS sustains.  A
+// (0.97 of them in a tile's union): 15.8 ms from idle, 17.9 ms back to back, where
+// the card sits at its power limit (1.55 GHz); 829 TFLOP/s of the formula's
+// five products, 1,275 of the products done, 0.92 of what cuBLAS sustains.  A
 // keys step is a chain of P, then dV and the next S: 2,650 cycles for 2,048 of
 // products; a queries step one of dS, then dQ and the next dP: 2,050 for 1,536.
 #include "lbsa_train_device.cuh"
@@ -69,7 +74,7 @@ struct Layout {
   static constexpr uint32_t ROWS1 = ACC2, ROWS2 = ACC2 + D / 2;      // queries: the tile's q and dout, two bf16 a column
   // shared memory
   static constexpr int TILE = BM * D * 2;                    // also a step's rows of one operand
-  static constexpr int OFF_R1 = 0, OFF_R2 = TILE;
+  static constexpr int OFF_R1 = 0, OFF_R2 = TILE;            // queries: KeyMean
   static constexpr int OFF_C1 = 2 * TILE, OFF_C2 = OFF_C1 + N1 * TILE;
   static constexpr int OFF_COL = OFF_C2 + N2 * TILE;         // per stage: BN lse, BN D
   static constexpr int OFF_BAR = OFF_COL + N2 * 2 * BN * 4;
@@ -396,8 +401,7 @@ __device__ __forceinline__ void keep_columns(uint32_t (&r)[kCols], uint32_t on, 
   }
 }
 // rounded to bf16, two a column
-__device__ __forceinline__ void store_packed(uint32_t taddr, const uint32_t (&r)[kCols]) {
-  uint32_t pk[kCols / 2];
+__device__ __forceinline__ void store_packed(uint32_t taddr, const uint32_t (&r)[kCols], uint32_t (&pk)[kCols / 2]) {
 #pragma unroll
   for (int c = 0; c < kCols / 2; ++c) pk[c] = pack_bf16x2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
   tmem_st16(taddr, pk);
@@ -431,6 +435,46 @@ __device__ __forceinline__ void own_rows(const Bars& bars, uint32_t tmem, const 
   warp_arrive(bars.r_full, threadIdx.x & 31);
 }
 
+// The mean of a query tile's kept keys: each slot of D / 4 threads adds every
+// SLOTS-th 64-row piece's sum.
+template <int D>
+struct KeyMean {
+  static constexpr int LANES = D / 4, SLOTS = kGroups * 128 / LANES;
+  float sums[SLOTS][D];
+  int rows[SLOTS];
+  float row_sums[kGroups][BM];       // of dS, as rounded
+  float mean[D];
+};
+static_assert(sizeof(KeyMean<64>) <= Layout<64, false>::TILE && sizeof(KeyMean<128>) <= Layout<128, false>::TILE, "in an operand's tile");
+template <int D>
+__device__ __forceinline__ void kept_keys(KeyMean<D>* m, const AttendGradArgs& a, const Tile& t, const uint32_t* row0,
+                                          const uint32_t* row1, int shift) {
+  const int lane = threadIdx.x % KeyMean<D>::LANES, slot = threadIdx.x / KeyMean<D>::LANES;
+  const float4* src = reinterpret_cast<const float4*>(a.k_sums + t.bh * (a.Npad / 64) * D) + lane;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  int rows = 0;
+  const int pieces = (a.N_valid + 63) >> 6;
+  for (int i0 = slot; i0 < pieces; i0 += 8 * KeyMean<D>::SLOTS) {
+    uint32_t on[8];                  // eight pieces' loads in flight
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * KeyMean<D>::SLOTS, block = i >> shift;
+      on[u] = i < pieces ? ((row0[block >> 5] | (row1 ? row1[block >> 5] : 0u)) >> (block & 31)) & 1u : 0u;
+    }
+    float4 x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      x[u] = on[u] ? src[static_cast<long long>(i0 + u * KeyMean<D>::SLOTS) * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      sum = make_float4(sum.x + x[u].x, sum.y + x[u].y, sum.z + x[u].z, sum.w + x[u].w);
+      rows += on[u] ? min(64, a.N_valid - (i0 + u * KeyMean<D>::SLOTS) * 64) : 0;
+    }
+  }
+  reinterpret_cast<float4*>(m->sums[slot])[lane] = sum;
+  if (lane == 0) m->rows[slot] = rows;
+}
+
 template <int D, bool KEYS, bool MASKED>
 __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_t tmem, const AttendGradArgs& a,
                                         const Tile& t, const uint32_t* entries, const CUtensorMap* out1,
@@ -449,6 +493,7 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
   }
   const uint64_t* sets = reinterpret_cast<const uint64_t*>(smem + L::OFF_SETS);
   bool alive = true;
+  float ds_sum[2] = {0.f, 0.f};       // queries: the row's rounded dS, two sums
   for (int j = 0; j < t.n_steps; ++j) {
     const int buf = j & (L::SB - 1);
     if (KEYS && L::SB == 2) {
@@ -482,7 +527,8 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
       keep_columns<MASKED && !KEYS>(r, on, e & kWhole);
     }
     if (KEYS) {
-      store_packed(s_col + buf * BN, r);
+      uint32_t pk[kCols / 2];
+      store_packed(s_col + buf * BN, r, pk);
       warp_arrive(bars.s_done + buf, lane);
     }
     alive = warp_wait(bars.dp_full, j & 1, wl, a.status, abort_flag);
@@ -491,8 +537,16 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
     tmem_ld32(dp_col, g);
     tmem_wait_ld_dep(g);
     score_gradients<KEYS>(g, r, col + BN, neg_delta);                // 0 where P is
-    store_packed(dp_col, g);
+    uint32_t pk[kCols / 2];
+    store_packed(dp_col, g, pk);
     warp_arrive(bars.ds_full, lane);
+    if (!KEYS) {
+#pragma unroll
+      for (int c = 0; c < kCols / 2; ++c)
+        asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\nadd.rn.f32.bf16 %0, l, %0;\nadd.rn.f32.bf16 %1, h, %1;\n}"
+            : "+f"(ds_sum[0]), "+f"(ds_sum[1])
+            : "r"(pk[c]));
+    }
   }
   // ---- the rows' sums
   bool sums = alive && t.n_steps > 0;
@@ -507,6 +561,25 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
   // dv of d = 128.)
   constexpr int PANELS = (KEYS ? 2 : 1) * (D / 64);
   const int pr = wg >> 1;
+  KeyMean<D>* m = reinterpret_cast<KeyMean<D>*>(smem + L::OFF_R1);
+  float off_zero = 0.f;
+  if (!KEYS) {
+    m->row_sums[wg][row] = ds_sum[0] + ds_sum[1];
+    named_bar_sync(4, kGroups * 128);
+    if (threadIdx.x < D) {
+      float sum = 0.f;
+      int rows = 0;
+#pragma unroll
+      for (int i = 0; i < KeyMean<D>::SLOTS; ++i) {
+        sum += m->sums[i][threadIdx.x];
+        rows += m->rows[i];
+      }
+      m->mean[threadIdx.x] = rows ? sum / static_cast<float>(rows) : 0.f;
+    }
+    named_bar_sync(4, kGroups * 128);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) off_zero += m->row_sums[i][row];
+  }
   for (int i = pr; i < PANELS; i += 2) {
     const int acc = i / (D / 64), c64 = (i % (D / 64)) * 64;
     const float f = KEYS && acc == 1 ? 1.f : scale;
@@ -517,6 +590,11 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
     } else {
 #pragma unroll
       for (int j = 0; j < 32; ++j) o[j] = 0u;
+    }
+    if (!KEYS && sums) {
+      const float* mean = m->mean + c64 + (wg & 1) * 32;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(fmaf(-off_zero, mean[j], __uint_as_float(o[j])));
     }
     uint8_t* panel = smem + L::OFF_C1 + i * BM * 128;
 #pragma unroll
@@ -599,6 +677,7 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
       else produce<D, KEYS, MASKED>(smem, bars, tk, tv, a, t, walk, entries, abort_flag);
     }
   } else {
+    if (!KEYS && warp < kProducer) kept_keys<D>(reinterpret_cast<KeyMean<D>*>(smem + L::OFF_R1), a, t, row0, row1, shift);
     if (threadIdx.x < 128) {
       int n = 0;
       for (int w = threadIdx.x; w < W; w += 128) n += __popc(row0[w] | (row1 ? row1[w] : 0u));

@@ -705,13 +705,13 @@ int lbsa_attend_backward(const void* q, const void* k, const void* v, const void
   if (dev != bs->device) return fail(LBSA_ERR_INVALID_ARG, "blockset lives on device %d, current is %d", bs->device, dev);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   lbsa::AttendGradArgs a{desc->B, desc->H, desc->N_valid, desc->d, bs->block, bs->nB, bs->counts, bs->cols, bs->masks,
-                         bs->status, q, dout, dq, dk, dv, {}, wait_limit()};
+                         bs->status, q, k, dout, dq, dk, dv, {}, wait_limit()};
   for (int i = 0; i < lbsa::kGradTensors; ++i) a.st[i] = st[i];
   DeviceState* ds = nullptr;
   Scratch ws;
   if ((rc = device_state(&ds)) != LBSA_OK) return rc;
-  if ((rc = scratch_alloc(ds, lbsa::attend_grad_workspace(&a, nullptr), s, &ws)) != LBSA_OK) return rc;
-  lbsa::attend_grad_workspace(&a, ws.ptr);
+  if ((rc = scratch_alloc(ds, lbsa::attend_grad_workspace(&a, desc->dtype, nullptr), s, &ws)) != LBSA_OK) return rc;
+  lbsa::attend_grad_workspace(&a, desc->dtype, ws.ptr);
   CUtensorMap maps[7];
   if (desc->dtype == LBSA_BF16) {
     const int which[7] = {lbsa::kQ, lbsa::kK, lbsa::kV, lbsa::kDout, lbsa::kDq, lbsa::kDk, lbsa::kDv};

@@ -42,7 +42,7 @@ struct AttendGradArgs {
   const int32_t* cols;
   const uint64_t* masks;        // per-token scope, as AttendArgs::masks
   int32_t* status;
-  const void *q, *dout;         // a query tile's own rows are read without a tensor map
+  const void *q, *k, *dout;     // bf16: a query tile's own rows are read without a tensor map, k's sums taken
   void *dq, *dk, *dv;           // fp32; bf16 gradients leave through tensor maps
   GradStride st[kGradTensors];
   long long wait_limit;
@@ -50,12 +50,13 @@ struct AttendGradArgs {
   int Npad;                     // N_valid rounded up to whole 128-row tiles
   float* neg_lse2;              // [B*H][Npad] -lse in log2 units; -inf: the row keeps nothing
   float* neg_delta;             // [B*H][Npad] -sum of dout * out
+  float* k_sums;                // bf16: [B*H][Npad / 64][d] k summed over each 64 rows
   uint32_t* bits;               // [B*H][nB queries][ceil(nB / 32)] kept key blocks
   uint32_t* bits_t;             // [B*H][nB keys][ceil(nB / 32)] query blocks that keep it
   uint64_t* masks_t;            // [B*H][nB keys][nB queries], written where bits are set
 };
 // sets Npad and, with base, the table pointers; returns the bytes wanted
-size_t attend_grad_workspace(AttendGradArgs* a, void* base);
+size_t attend_grad_workspace(AttendGradArgs* a, int dtype, void* base);
 cudaError_t launch_attend_grad_prep(const void* out, const void* dout, const float* lse, int dtype,
                                     const AttendGradArgs& a, cudaStream_t s);
 // bf16 on the tensor cores (attend_grad_tc.cu); in: q, k, v, dout with boxes of

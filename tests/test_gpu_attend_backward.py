@@ -78,7 +78,18 @@ def _reference(q, k, v, dout, pairs, dtype):
     de = (a(dout) * oe).sum(-1, keepdims=True) + d * E * (a(dout) * a(out)).sum(-1, keepdims=True)
     dse = (pe + hp) * a(ds) + p * (de + d * E * (a(dout) @ t(a(v))))
     n = N * E
-    bounds = (scale * ((dse + n * a(ds)) @ a(k)) + h * a(grads[0]), scale * (t(dse + n * a(ds)) @ a(q)) + h * a(grads[1]),
+    # bf16: dq is summed as sum_c dS_rc (k_c - m), the same number for any m since sum_c dS_rc = 0, with m the mean
+    # key of the 64-row pieces that the row's 128-row tile keeps: an error of dS_rc counts |k_c - m|, the fp32 sums
+    # are of |dS_rc| |k_c| and |dS_rc| |m|
+    dq_bound = np.empty_like(q)
+    for t0 in range(0, N, 128):
+        rows, m = slice(t0, t0 + 128), 0.0
+        if dtype == torch.bfloat16:
+            on = np.add.reduceat(pairs[:, :, rows].any(2), np.arange(0, N, 64), axis=-1) > 0
+            on = np.repeat(on, 64, -1)[..., :N, None]
+            m = ((on * k).sum(2) / np.maximum(on.sum(2), 1))[:, :, None]
+        dq_bound[:, :, rows] = scale * (dse[:, :, rows] @ a(k - m) + n * a(ds[:, :, rows]) @ (a(k) + a(m)))
+    bounds = (dq_bound + h * a(grads[0]), scale * (t(dse + n * a(ds)) @ a(q)) + h * a(grads[1]),
               t(p * (pe + hp + n)) @ a(dout) + h * a(grads[2]))
     return grads, bounds
 
@@ -146,6 +157,19 @@ def test_sharp_and_flat_rows(dtype):
     keep = _keep(5, 1, 2, 5, 5, 0.7)
     _run(1, 2, 290, 128, 64, dtype, keep, seed=5, sharp=12.0)     # logits to about 40: one key takes nearly all
     _run(1, 2, 290, 128, 64, dtype, keep, seed=5, sharp=0.0)      # equal logits
+
+
+@BOTH
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_with_much_in_common(d, dtype):
+    # sum_c dS_rc = 0 takes the common part out of dq; roundings of dS must not bring it back
+    B, H, N, keep = 1, 2, 400, _keep(4, 1, 2, 7, 7, 0.6)
+    q, k, v, dout = (_normal(4 + i, B, H, N, d, dtype=dtype) for i in range(4))
+    k = (k + 20 * _normal(3, d)).to(dtype)
+    bs = _blockset(keep, 64)
+    out, lse = lbsa.lbsa_attend(q, k, v, bs, want_lse=True)
+    got = lbsa.lbsa_attend_backward(q, k, v, bs, out, lse, dout)
+    _check(got, *_reference(q, k, v, dout, _pairs(keep, N, 64, False), dtype))
 
 
 @BOTH
