@@ -31,9 +31,11 @@
 // fp32.  D is taken from the rounded out.  sum_c dS_rc = 0 takes out of dq what
 // the keys have in common, but rounded dS sum to some e_r, which would bring it
 // back.  So dq_r = scale sum_c dS_rc (k_c - m), the same number for any m: m is
-// the mean of the tile's kept keys, and e_r m is taken off at the end.  Keys of
-// unit noise about a common vector of its size: dq 2.4e-3 off (Frobenius),
-// 3.4e-3 without m, where rounding the exact result costs 1.7e-3.  e_r adds a
+// the mean key at the tile's own place, which the near keys that a row looks at
+// most are like, and e_r m is taken off at the end.  Keys of unit noise about a
+// common vector of its size, or about one that goes along the clip: dq 2.4e-3
+// off (Frobenius), 3.4e-3 without m (with the mean of all kept keys 2.4e-3 and
+// 3.4e-3), where rounding the exact result costs 1.7e-3.  e_r adds a
 // mixed fp32 + bf16 addition an element, the rest little: 17.6 -> 17.9 ms below,
 // 0.1375 -> 0.1456 ms for 4,884 tokens, 128-token blocks, d = 64 (with the pairs
 // unpacked and added as fp32x2: 18.2 and 0.149 ms).
@@ -435,8 +437,9 @@ __device__ __forceinline__ void own_rows(const Bars& bars, uint32_t tmem, const 
   warp_arrive(bars.r_full, threadIdx.x & 31);
 }
 
-// The mean of a query tile's kept keys: each slot of D / 4 threads adds every
-// SLOTS-th 64-row piece's sum.
+// The mean of the keys at a query tile's own place, as far as it keeps them, and
+// of all that it keeps where it keeps neither piece: each slot of D / 4 threads
+// adds every SLOTS-th 64-row piece's sum.
 template <int D>
 struct KeyMean {
   static constexpr int LANES = D / 4, SLOTS = kGroups * 128 / LANES;
@@ -453,13 +456,19 @@ __device__ __forceinline__ void kept_keys(KeyMean<D>* m, const AttendGradArgs& a
   const float4* src = reinterpret_cast<const float4*>(a.k_sums + t.bh * (a.Npad / 64) * D) + lane;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   int rows = 0;
-  const int pieces = (a.N_valid + 63) >> 6;
-  for (int i0 = slot; i0 < pieces; i0 += 8 * KeyMean<D>::SLOTS) {
+  const int pieces = (a.N_valid + 63) >> 6, own = t.tile * 2;
+  auto kept = [&](int i) {
+    const int block = i >> shift;
+    return i < pieces ? ((row0[block >> 5] | (row1 ? row1[block >> 5] : 0u)) >> (block & 31)) & 1u : 0u;
+  };
+  const bool mine = kept(own) | kept(own + 1);
+  const int end = mine ? min(pieces, own + 2) : pieces;
+  for (int i0 = slot + (mine ? own : 0); i0 < end; i0 += 8 * KeyMean<D>::SLOTS) {
     uint32_t on[8];                  // eight pieces' loads in flight
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int i = i0 + u * KeyMean<D>::SLOTS, block = i >> shift;
-      on[u] = i < pieces ? ((row0[block >> 5] | (row1 ? row1[block >> 5] : 0u)) >> (block & 31)) & 1u : 0u;
+      const int i = i0 + u * KeyMean<D>::SLOTS;
+      on[u] = i < end ? kept(i) : 0u;
     }
     float4 x[8];
 #pragma unroll
