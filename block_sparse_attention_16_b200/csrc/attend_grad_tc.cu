@@ -31,8 +31,8 @@
 // fp32.  D is taken from the rounded out.  sum_c dS_rc = 0 takes out of dq what
 // the keys have in common, but rounded dS sum to some e_r, which would bring it
 // back.  So dq_r = scale sum_c dS_rc (k_c - m), the same number for any m: m is
-// the mean key at the tile's own place, which the near keys that a row looks at
-// most are like, and e_r m is taken off at the end.  Keys of unit noise about a
+// the mean of the 64 keys at the row's own place, which the near keys that it looks
+// at most are like, and e_r m is taken off at the end.  Keys of unit noise about a
 // common vector of its size, or about one that goes along the clip: dq 2.4e-3
 // off (Frobenius), 3.4e-3 without m (with the mean of all kept keys 2.4e-3 and
 // 3.4e-3), where rounding the exact result costs 1.7e-3.  e_r adds a
@@ -437,16 +437,17 @@ __device__ __forceinline__ void own_rows(const Bars& bars, uint32_t tmem, const 
   warp_arrive(bars.r_full, threadIdx.x & 31);
 }
 
-// The mean of the keys at a query tile's own place, as far as it keeps them, and
-// of all that it keeps where it keeps neither piece: each slot of D / 4 threads
-// adds every SLOTS-th 64-row piece's sum.
+// For each half of a query tile the mean of the 64 keys at its own place, where
+// the tile keeps them, and of all that the tile keeps where it does not: each slot
+// of D / 4 threads adds every SLOTS-th 64-row piece's sum.
 template <int D>
 struct KeyMean {
   static constexpr int LANES = D / 4, SLOTS = kGroups * 128 / LANES;
   float sums[SLOTS][D];
   int rows[SLOTS];
+  uint32_t mine[2];                  // the half keeps its own place: its mean stands
   float row_sums[kGroups][BM];       // of dS, as rounded
-  float mean[D];
+  float mean[2][D];
 };
 static_assert(sizeof(KeyMean<64>) <= Layout<64, false>::TILE && sizeof(KeyMean<128>) <= Layout<128, false>::TILE, "in an operand's tile");
 template <int D>
@@ -461,14 +462,20 @@ __device__ __forceinline__ void kept_keys(KeyMean<D>* m, const AttendGradArgs& a
     const int block = i >> shift;
     return i < pieces ? ((row0[block >> 5] | (row1 ? row1[block >> 5] : 0u)) >> (block & 31)) & 1u : 0u;
   };
-  const bool mine = kept(own) | kept(own + 1);
-  const int end = mine ? min(pieces, own + 2) : pieces;
-  for (int i0 = slot + (mine ? own : 0); i0 < end; i0 += 8 * KeyMean<D>::SLOTS) {
+  // the second half may have no rows
+  const bool all = !kept(own) || (own + 1 < pieces && !kept(own + 1));
+  if (threadIdx.x < 2 * D) {
+    const int i = own + threadIdx.x / D;
+    if (kept(i))
+      m->mean[threadIdx.x / D][threadIdx.x % D] =
+          a.k_sums[(t.bh * (a.Npad / 64) + i) * D + threadIdx.x % D] / static_cast<float>(min(64, a.N_valid - i * 64));
+  }
+  for (int i0 = slot; all && i0 < pieces; i0 += 8 * KeyMean<D>::SLOTS) {
     uint32_t on[8];                  // eight pieces' loads in flight
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int i = i0 + u * KeyMean<D>::SLOTS;
-      on[u] = i < end ? kept(i) : 0u;
+      on[u] = kept(i);
     }
     float4 x[8];
 #pragma unroll
@@ -482,6 +489,7 @@ __device__ __forceinline__ void kept_keys(KeyMean<D>* m, const AttendGradArgs& a
   }
   reinterpret_cast<float4*>(m->sums[slot])[lane] = sum;
   if (lane == 0) m->rows[slot] = rows;
+  if (threadIdx.x < 2) m->mine[threadIdx.x] = kept(own + threadIdx.x);
 }
 
 template <int D, bool KEYS, bool MASKED>
@@ -575,15 +583,16 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
   if (!KEYS) {
     m->row_sums[wg][row] = ds_sum[0] + ds_sum[1];
     named_bar_sync(4, kGroups * 128);
-    if (threadIdx.x < D) {
+    if (threadIdx.x < 2 * D && !m->mine[threadIdx.x / D]) {
+      const int c = threadIdx.x % D;
       float sum = 0.f;
       int rows = 0;
 #pragma unroll
       for (int i = 0; i < KeyMean<D>::SLOTS; ++i) {
-        sum += m->sums[i][threadIdx.x];
+        sum += m->sums[i][c];
         rows += m->rows[i];
       }
-      m->mean[threadIdx.x] = rows ? sum / static_cast<float>(rows) : 0.f;
+      m->mean[threadIdx.x / D][c] = rows ? sum / static_cast<float>(rows) : 0.f;
     }
     named_bar_sync(4, kGroups * 128);
 #pragma unroll
@@ -601,7 +610,7 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
       for (int j = 0; j < 32; ++j) o[j] = 0u;
     }
     if (!KEYS && sums) {
-      const float* mean = m->mean + c64 + (wg & 1) * 32;
+      const float* mean = m->mean[half] + c64 + (wg & 1) * 32;
 #pragma unroll
       for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(fmaf(-off_zero, mean[j], __uint_as_float(o[j])));
     }

@@ -79,15 +79,16 @@ def _reference(q, k, v, dout, pairs, dtype):
     dse = (pe + hp) * a(ds) + p * (de + d * E * (a(dout) @ t(a(v))))
     n = N * E
     # bf16: dq is summed as sum_c dS_rc (k_c - m), the same number for any m since sum_c dS_rc = 0, with m the mean
-    # key of the 64-row pieces that the row's 128-row tile keeps, only of those at its own place if there is one: an
-    # error of dS_rc counts |k_c - m|, the fp32 sums are of |dS_rc| |k_c| and |dS_rc| |m|
+    # of the 64 keys at the row's own place if its 128-row tile keeps them, else of all that the tile keeps: an error
+    # of dS_rc counts |k_c - m|, the fp32 sums are of |dS_rc| |k_c| and |dS_rc| |m|
     dq_bound = np.empty_like(q)
-    for t0 in range(0, N, 128):
-        rows, m = slice(t0, t0 + 128), 0.0
+    for t0 in range(0, N, 64):
+        rows, m = slice(t0, t0 + 64), 0.0
         if dtype == torch.bfloat16:
-            on = np.add.reduceat(pairs[:, :, rows].any(2), np.arange(0, N, 64), axis=-1) > 0
-            own = on.copy()
-            own[..., :t0 // 64] = own[..., t0 // 64 + 2:] = False
+            tile = slice(t0 // 128 * 128, t0 // 128 * 128 + 128)
+            on = np.add.reduceat(pairs[:, :, tile].any(2), np.arange(0, N, 64), axis=-1) > 0
+            own = np.zeros_like(on)
+            own[..., t0 // 64] = on[..., t0 // 64]
             on = np.where(own.any(-1, keepdims=True), own, on)
             on = np.repeat(on, 64, -1)[..., :N, None]
             m = ((on * k).sum(2) / np.maximum(on.sum(2), 1))[:, :, None]
