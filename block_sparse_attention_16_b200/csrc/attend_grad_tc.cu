@@ -31,19 +31,19 @@
 // fp32.  D is taken from the rounded out.  sum_c dS_rc = 0 takes out of dq what
 // the keys have in common, but rounded dS sum to some e_r, which would bring it
 // back.  So dq_r = scale sum_c dS_rc (k_c - m), the same number for any m: m is
-// the mean of the 64 keys at the row's own place, which the near keys that it looks
-// at most are like, and e_r m is taken off at the end.  Keys of unit noise about a
-// common vector of its size, or about one that goes along the clip: dq 2.4e-3
-// off (Frobenius), 3.4e-3 without m (with the mean of all kept keys 2.4e-3 and
-// 3.4e-3), where rounding the exact result costs 1.7e-3.  e_r adds a
-// mixed fp32 + bf16 addition an element, the rest little: 17.6 -> 17.9 ms below,
-// 0.1375 -> 0.1456 ms for 4,884 tokens, 128-token blocks, d = 64 (with the pairs
+// the mean of the nearest 64 keys that the tile keeps, as near keys are looked at
+// most, and e_r m is taken off at the end.  Keys of unit noise about a common
+// vector of that size, or about one that changes along the clip: dq 2.4e-3 to
+// 2.5e-3 off (Frobenius), 3.4e-3 without m, where rounding the exact result
+// costs 1.7e-3; the mean of all kept keys mends the first only.  e_r adds a
+// mixed fp32 + bf16 addition an element, the rest little: 17.6 -> 17.8 ms below,
+// 0.138 -> 0.145 ms for 4,884 tokens, 128-token blocks, d = 64 (with the pairs
 // unpacked and added as fp32x2: 18.2 and 0.149 ms).
 //
 // What bounds it: 21 x 30 x 52 tokens, 12 heads of 128, 0.90 of the blocks kept
-// (0.97 of them in a tile's union): 15.8 ms from idle, 17.9 ms back to back, where
-// the card sits at its power limit (1.55 GHz); 829 TFLOP/s of the formula's
-// five products, 1,275 of the products done, 0.92 of what cuBLAS sustains.  A
+// (0.97 of them in a tile's union): 16.0 ms from idle, 17.8 ms back to back, where
+// the card sits at its power limit (1.55 GHz); 833 TFLOP/s of the formula's
+// five products, 1,280 of the products done, 0.92 of what cuBLAS sustains.  A
 // keys step is a chain of P, then dV and the next S: 2,650 cycles for 2,048 of
 // products; a queries step one of dS, then dQ and the next dP: 2,050 for 1,536.
 #include "lbsa_train_device.cuh"
@@ -437,59 +437,32 @@ __device__ __forceinline__ void own_rows(const Bars& bars, uint32_t tmem, const 
   warp_arrive(bars.r_full, threadIdx.x & 31);
 }
 
-// For each half of a query tile the mean of the 64 keys at its own place, where
-// the tile keeps them, and of all that the tile keeps where it does not: each slot
-// of D / 4 threads adds every SLOTS-th 64-row piece's sum.
+// For each half of a query tile the mean of a piece that the tile keeps, the
+// nearest to the half's own place.
 template <int D>
 struct KeyMean {
-  static constexpr int LANES = D / 4, SLOTS = kGroups * 128 / LANES;
-  float sums[SLOTS][D];
-  int rows[SLOTS];
-  uint32_t mine[2];                  // the half keeps its own place: its mean stands
   float row_sums[kGroups][BM];       // of dS, as rounded
   float mean[2][D];
 };
 static_assert(sizeof(KeyMean<64>) <= Layout<64, false>::TILE && sizeof(KeyMean<128>) <= Layout<128, false>::TILE, "in an operand's tile");
+// two warps, one a half
 template <int D>
-__device__ __forceinline__ void kept_keys(KeyMean<D>* m, const AttendGradArgs& a, const Tile& t, const uint32_t* row0,
-                                          const uint32_t* row1, int shift) {
-  const int lane = threadIdx.x % KeyMean<D>::LANES, slot = threadIdx.x / KeyMean<D>::LANES;
-  const float4* src = reinterpret_cast<const float4*>(a.k_sums + t.bh * (a.Npad / 64) * D) + lane;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  int rows = 0;
-  const int pieces = (a.N_valid + 63) >> 6, own = t.tile * 2;
+__device__ __forceinline__ void nearest_keys(KeyMean<D>* m, const AttendGradArgs& a, const Tile& t, const uint32_t* row0,
+                                             const uint32_t* row1, int shift) {
+  const int lane = threadIdx.x & 31, half = threadIdx.x >> 5, own = t.tile * 2 + half, pieces = (a.N_valid + 63) >> 6;
   auto kept = [&](int i) {
     const int block = i >> shift;
-    return i < pieces ? ((row0[block >> 5] | (row1 ? row1[block >> 5] : 0u)) >> (block & 31)) & 1u : 0u;
+    return i >= 0 && i < pieces && (((row0[block >> 5] | (row1 ? row1[block >> 5] : 0u)) >> (block & 31)) & 1u);
   };
-  // the second half may have no rows
-  const bool all = !kept(own) || (own + 1 < pieces && !kept(own + 1));
-  if (threadIdx.x < 2 * D) {
-    const int i = own + threadIdx.x / D;
-    if (kept(i))
-      m->mean[threadIdx.x / D][threadIdx.x % D] =
-          a.k_sums[(t.bh * (a.Npad / 64) + i) * D + threadIdx.x % D] / static_cast<float>(min(64, a.N_valid - i * 64));
+  int at = -1;
+  for (int away = lane; at < 0 && away - lane <= pieces; away += 32) {
+    const bool after = kept(own + away), before = kept(own - away);
+    const uint32_t found = __ballot_sync(0xffffffffu, after || before);
+    if (found) at = __shfl_sync(0xffffffffu, after ? own + away : own - away, __ffs(found) - 1);
   }
-  for (int i0 = slot; all && i0 < pieces; i0 += 8 * KeyMean<D>::SLOTS) {
-    uint32_t on[8];                  // eight pieces' loads in flight
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = i0 + u * KeyMean<D>::SLOTS;
-      on[u] = kept(i);
-    }
-    float4 x[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      x[u] = on[u] ? src[static_cast<long long>(i0 + u * KeyMean<D>::SLOTS) * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      sum = make_float4(sum.x + x[u].x, sum.y + x[u].y, sum.z + x[u].z, sum.w + x[u].w);
-      rows += on[u] ? min(64, a.N_valid - (i0 + u * KeyMean<D>::SLOTS) * 64) : 0;
-    }
-  }
-  reinterpret_cast<float4*>(m->sums[slot])[lane] = sum;
-  if (lane == 0) m->rows[slot] = rows;
-  if (threadIdx.x < 2) m->mine[threadIdx.x] = kept(own + threadIdx.x);
+  const float r = at < 0 ? 0.f : 1.f / static_cast<float>(min(64, a.N_valid - at * 64));
+  for (int c = lane; c < D; c += 32)
+    m->mean[half][c] = at < 0 ? 0.f : a.k_sums[(t.bh * (a.Npad / 64) + at) * D + c] * r;
 }
 
 template <int D, bool KEYS, bool MASKED>
@@ -582,18 +555,6 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
   float off_zero = 0.f;
   if (!KEYS) {
     m->row_sums[wg][row] = ds_sum[0] + ds_sum[1];
-    named_bar_sync(4, kGroups * 128);
-    if (threadIdx.x < 2 * D && !m->mine[threadIdx.x / D]) {
-      const int c = threadIdx.x % D;
-      float sum = 0.f;
-      int rows = 0;
-#pragma unroll
-      for (int i = 0; i < KeyMean<D>::SLOTS; ++i) {
-        sum += m->sums[i][c];
-        rows += m->rows[i];
-      }
-      m->mean[threadIdx.x / D][c] = rows ? sum / static_cast<float>(rows) : 0.f;
-    }
     named_bar_sync(4, kGroups * 128);
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) off_zero += m->row_sums[i][row];
@@ -695,7 +656,7 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
       else produce<D, KEYS, MASKED>(smem, bars, tk, tv, a, t, walk, entries, abort_flag);
     }
   } else {
-    if (!KEYS && warp < kProducer) kept_keys<D>(reinterpret_cast<KeyMean<D>*>(smem + L::OFF_R1), a, t, row0, row1, shift);
+    if (!KEYS && warp < 2) nearest_keys<D>(reinterpret_cast<KeyMean<D>*>(smem + L::OFF_R1), a, t, row0, row1, shift);
     if (threadIdx.x < 128) {
       int n = 0;
       for (int w = threadIdx.x; w < W; w += 128) n += __popc(row0[w] | (row1 ? row1[w] : 0u));

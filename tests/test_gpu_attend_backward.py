@@ -79,17 +79,17 @@ def _reference(q, k, v, dout, pairs, dtype):
     dse = (pe + hp) * a(ds) + p * (de + d * E * (a(dout) @ t(a(v))))
     n = N * E
     # bf16: dq is summed as sum_c dS_rc (k_c - m), the same number for any m since sum_c dS_rc = 0, with m the mean
-    # of the 64 keys at the row's own place if its 128-row tile keeps them, else of all that the tile keeps: an error
-    # of dS_rc counts |k_c - m|, the fp32 sums are of |dS_rc| |k_c| and |dS_rc| |m|
+    # of the 64-row piece nearest to the row's own that its 128-row tile keeps (of two the later): an error of dS_rc
+    # counts |k_c - m|, the fp32 sums are of |dS_rc| |k_c| and |dS_rc| |m|
     dq_bound = np.empty_like(q)
     for t0 in range(0, N, 64):
         rows, m = slice(t0, t0 + 64), 0.0
         if dtype == torch.bfloat16:
             tile = slice(t0 // 128 * 128, t0 // 128 * 128 + 128)
             on = np.add.reduceat(pairs[:, :, tile].any(2), np.arange(0, N, 64), axis=-1) > 0
-            own = np.zeros_like(on)
-            own[..., t0 // 64] = on[..., t0 // 64]
-            on = np.where(own.any(-1, keepdims=True), own, on)
+            away = np.abs(np.arange(on.shape[-1]) - t0 // 64) * 2 + (np.arange(on.shape[-1]) < t0 // 64)
+            near = np.where(on, away, 1 << 30)
+            on = on & (near == near.min(-1, keepdims=True))
             on = np.repeat(on, 64, -1)[..., :N, None]
             m = ((on * k).sum(2) / np.maximum(on.sum(2), 1))[:, :, None]
         dq_bound[:, :, rows] = scale * (dse[:, :, rows] @ a(k - m) + n * a(ds[:, :, rows]) @ (a(k) + a(m)))
