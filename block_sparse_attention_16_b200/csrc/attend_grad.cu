@@ -14,9 +14,11 @@
 // give the same bits.
 //
 // Tables (scratch of the call): -lse in log2 units and -D, padded to whole
-// 128-row tiles (a row that keeps nothing, or does not exist, gets -inf and 0,
-// so that its P is 0 without a test), and the kept pairs as bits in
-// both directions; the per-token sets go to [key block][query block].
+// 128-row tiles (a row that keeps nothing, or does not exist, gets -inf and 0:
+// its P is 0, or 2^-125 where the bf16 kernel takes the exponential on the FMA
+// pipe, for which masks and the zeros read past the last row leave nothing), and
+// the kept pairs as bits in both directions; the per-token sets go to [key
+// block][query block].
 #include "lbsa_train_device.cuh"
 
 namespace lbsa {
@@ -51,8 +53,11 @@ constexpr int kRowsPerBlock = 64;        // query rows of a block of the second 
 
 // Blocks [0, index_blocks): 32 query blocks of one (batch, head) each, whose
 // lists become bit rows and, transposed in shared memory, one word of every
-// key block's bits.  The others: 64 rows each, D = dout . out and, bf16, the sum
-// of the key rows.  Bound by reading out, dout and k once.
+// key block's bits.  The others: 64 rows each, D = dout . out and, bf16, the
+// mean of the key rows if they have much in common: 0 unless |mean|^2 is more
+// than a quarter of what they vary by, so that a few keys far from the others
+// (fewer than a fifth of the 64), or infinite ones, are not taken for all of
+// them.  Bound by reading out, dout and k once.
 template <typename T, int D>
 __global__ void __launch_bounds__(kPrepThreads)
 attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, const float* __restrict__ lse,
@@ -134,7 +139,8 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
   }
   if constexpr (sizeof(T) == 2) {
     float* part = reinterpret_cast<float*>(bm);        // [GROUPS][D]
-    float s[8] = {};
+    __shared__ float squares[kPrepThreads / 32], mean_squares[D / 32];
+    float s[8] = {}, sq = 0.f;
 #pragma unroll
     for (int i = 0; i < kRowsPerBlock / GROUPS; ++i) {
       const int n = static_cast<int>(row0 + i * GROUPS + threadIdx.x / LANES - bh * a.Npad);
@@ -143,18 +149,40 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[2 * e] += __uint_as_float(w[e] << 16);
-        s[2 * e + 1] += __uint_as_float(w[e] & 0xFFFF0000u);
+        const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xFFFF0000u);
+        s[2 * e] += lo;
+        s[2 * e + 1] += hi;
+        sq = fmaf(lo, lo, fmaf(hi, hi, sq));
       }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) part[threadIdx.x / LANES * D + lane * 8 + e] = s[e];
+    auto warp_sum = [](float v) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      return v;
+    };
+    sq = warp_sum(sq);
+    if ((threadIdx.x & 31) == 0) squares[threadIdx.x >> 5] = sq;
+    __syncthreads();
+    constexpr float R = 1.f / kRowsPerBlock;           // a ragged piece's mean is not used
+    float mean = 0.f;
+    if (threadIdx.x < D) {
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) mean += part[g * D + threadIdx.x];
+      mean *= R;
+      const float m2 = warp_sum(mean * mean);
+      if ((threadIdx.x & 31) == 0) mean_squares[threadIdx.x >> 5] = m2;
+    }
     __syncthreads();
     if (threadIdx.x < D) {
-      float t = 0.f;
+      float m2 = 0.f, all = 0.f;
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g) t += part[g * D + threadIdx.x];
-      a.k_sums[row0 / kRowsPerBlock * D + threadIdx.x] = t;
+      for (int i = 0; i < D / 32; ++i) m2 += mean_squares[i];
+#pragma unroll
+      for (int i = 0; i < kPrepThreads / 32; ++i) all += squares[i];
+      // false where a sum is not finite, too
+      a.k_means[row0 / kRowsPerBlock * D + threadIdx.x] = 4.f * m2 > all * R - m2 ? mean : 0.f;
     }
   }
 }
@@ -476,7 +504,7 @@ size_t attend_grad_workspace(AttendGradArgs* a, int dtype, void* base) {
   p[4] = a->masks ? take(bh * a->nB * a->nB * sizeof(uint64_t)) : nullptr;
   p[5] = dtype == LBSA_BF16 ? take(bh * (a->Npad / kRowsPerBlock) * a->d * sizeof(float)) : nullptr;
   if (base) {
-    a->k_sums = reinterpret_cast<float*>(p[5]);
+    a->k_means = reinterpret_cast<float*>(p[5]);
     a->neg_lse2 = reinterpret_cast<float*>(p[0]);
     a->neg_delta = reinterpret_cast<float*>(p[1]);
     a->bits = reinterpret_cast<uint32_t*>(p[2]);

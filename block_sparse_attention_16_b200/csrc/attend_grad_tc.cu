@@ -27,23 +27,29 @@
 // product reads 8 KB in the 64 cycles that the tensor core needs for it, the
 // whole bandwidth, and took 90 to 100 cycles.
 //
-// Roundings: P and dS become bf16 once, as operands (2^-9 relative); all else is
-// fp32.  D is taken from the rounded out.  sum_c dS_rc = 0 takes out of dq what
-// the keys have in common, but rounded dS sum to some e_r, which would bring it
-// back.  So dq_r = scale sum_c dS_rc (k_c - m), the same number for any m: m is
-// the mean of the nearest 64 keys that the tile keeps, as near keys are looked at
-// most, and e_r m is taken off at the end.  Keys of unit noise about a common
-// vector of that size, or about one that changes along the clip: dq 2.4e-3 to
-// 2.5e-3 off (Frobenius), 3.4e-3 without m, where rounding the exact result
-// costs 1.7e-3; the mean of all kept keys mends the first only.  e_r adds a
-// mixed fp32 + bf16 addition an element, the rest little: 17.6 -> 17.8 ms below,
-// 0.138 -> 0.145 ms for 4,884 tokens, 128-token blocks, d = 64 (with the pairs
-// unpacked and added as fp32x2: 18.2 and 0.149 ms).
+// Roundings: P and dS become bf16 once, as operands (2^-8 relative at most); all
+// else is fp32.  D is taken from the rounded out.  sum_c dS_rc = 0 takes out of dq
+// what the keys have in common, but rounded dS sum to some e_r, which would bring
+// it back.  So dq_r = scale sum_c dS_rc (k_c - m_r), the same number for any m_r,
+// and e_r m_r is taken off at the end.  What is best taken off is the row's own
+// mean key, sum_c P_rc k_c, a fourth product; m_r stands near it and is read from
+// a table: the mean of the 64 keys among which the row's largest P is, 0 where
+// those have little in common (attend_grad_prep_kernel), or that P's own key where
+// it takes half of the row or its piece is ragged.  Keys that the row does not
+// keep, or gives no P, have no part in it, whatever their size.  dq off by
+// (Frobenius; 4,096 tokens, d = 128, half of the blocks; rounding the exact result
+// costs 1.7e-3): keys of unit noise 2.4e-3, about a common vector of 1 or of 20
+// times that size 2.4e-3 (without m_r 3.2e-3 and 4.5e-2), about one that changes
+// along the clip 2.5e-3, about a vector for each block of 1 to 20 times that size
+// 2.9e-3 to 3.4e-3 (without 2.7e-3 to 1.3e-2; with the nearest kept piece's mean
+// 3.3e-3 to 1.9e-2), logits of deviation 12 2.9e-3.  e_r takes a mixed fp32 + bf16
+// addition an element, the largest P half a three-way maximum: 0.5 % of the
+// time below.
 //
 // What bounds it: 21 x 30 x 52 tokens, 12 heads of 128, 0.90 of the blocks kept
-// (0.97 of them in a tile's union): 16.0 ms from idle, 17.8 ms back to back, where
-// the card sits at its power limit (1.55 GHz); 833 TFLOP/s of the formula's
-// five products, 1,280 of the products done, 0.92 of what cuBLAS sustains.  A
+// (0.97 of them in a tile's union): 16.1 ms from idle, 18.3 ms back to back, where
+// the card sits at its power limit (1.55 GHz); 810 TFLOP/s of the formula's
+// five products, 1,220 of the products done, 0.88 of what cuBLAS sustains.  A
 // keys step is a chain of P, then dV and the next S: 2,650 cycles for 2,048 of
 // products; a queries step one of dS, then dQ and the next dP: 2,050 for 1,536.
 #include "lbsa_train_device.cuh"
@@ -56,7 +62,7 @@ constexpr int kCols = 32;           // columns of a step that a softmax warpgrou
 constexpr int N1 = 3, N2 = 2;       // ring depths of the two operands
 // Of every 8 groups of four logits kPoly8 take two of their exponentials on the
 // FMA pipe (a cubic, relative error 7.5e-5, far below the rounding of P and dS
-// to bf16, 2^-9), which unloads the MUFU: with 4 (a quarter of them) 8,192
+// to bf16, 2^-8), which unloads the MUFU: with 4 (a quarter of them) 8,192
 // dense tokens of 8 heads of 64 took 0.59 ms, with none 0.61.
 constexpr int kPoly8 = 4;
 constexpr int BN = 128;             // columns of a step, two 64-row pieces
@@ -76,7 +82,7 @@ struct Layout {
   static constexpr uint32_t ROWS1 = ACC2, ROWS2 = ACC2 + D / 2;      // queries: the tile's q and dout, two bf16 a column
   // shared memory
   static constexpr int TILE = BM * D * 2;                    // also a step's rows of one operand
-  static constexpr int OFF_R1 = 0, OFF_R2 = TILE;            // queries: KeyMean
+  static constexpr int OFF_R1 = 0, OFF_R2 = TILE;            // queries: RowParts
   static constexpr int OFF_C1 = 2 * TILE, OFF_C2 = OFF_C1 + N1 * TILE;
   static constexpr int OFF_COL = OFF_C2 + N2 * TILE;         // per stage: BN lse, BN D
   static constexpr int OFF_BAR = OFF_COL + N2 * 2 * BN * 4;
@@ -437,33 +443,13 @@ __device__ __forceinline__ void own_rows(const Bars& bars, uint32_t tmem, const 
   warp_arrive(bars.r_full, threadIdx.x & 31);
 }
 
-// For each half of a query tile the mean of a piece that the tile keeps, the
-// nearest to the half's own place.
-template <int D>
-struct KeyMean {
-  float row_sums[kGroups][BM];       // of dS, as rounded
-  float mean[2][D];
+// What the four warpgroups know of a query row, each from its columns.
+struct RowParts {
+  float sum[kGroups][BM];           // of dS, as rounded
+  float top[kGroups][BM];           // the largest P
+  int at[kGroups][BM];              // its piece; ~its key where P is half of the row's or more, or the piece ragged
 };
-static_assert(sizeof(KeyMean<64>) <= Layout<64, false>::TILE && sizeof(KeyMean<128>) <= Layout<128, false>::TILE, "in an operand's tile");
-// two warps, one a half
-template <int D>
-__device__ __forceinline__ void nearest_keys(KeyMean<D>* m, const AttendGradArgs& a, const Tile& t, const uint32_t* row0,
-                                             const uint32_t* row1, int shift) {
-  const int lane = threadIdx.x & 31, half = threadIdx.x >> 5, own = t.tile * 2 + half, pieces = (a.N_valid + 63) >> 6;
-  auto kept = [&](int i) {
-    const int block = i >> shift;
-    return i >= 0 && i < pieces && (((row0[block >> 5] | (row1 ? row1[block >> 5] : 0u)) >> (block & 31)) & 1u);
-  };
-  int at = -1;
-  for (int away = lane; at < 0 && away - lane <= pieces; away += 32) {
-    const bool after = kept(own + away), before = kept(own - away);
-    const uint32_t found = __ballot_sync(0xffffffffu, after || before);
-    if (found) at = __shfl_sync(0xffffffffu, after ? own + away : own - away, __ffs(found) - 1);
-  }
-  const float r = at < 0 ? 0.f : 1.f / static_cast<float>(min(64, a.N_valid - at * 64));
-  for (int c = lane; c < D; c += 32)
-    m->mean[half][c] = at < 0 ? 0.f : a.k_sums[(t.bh * (a.Npad / 64) + at) * D + c] * r;
-}
+static_assert(sizeof(RowParts) <= Layout<64, false>::TILE, "in an operand's tile");
 
 template <int D, bool KEYS, bool MASKED>
 __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_t tmem, const AttendGradArgs& a,
@@ -484,6 +470,8 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
   const uint64_t* sets = reinterpret_cast<const uint64_t*>(smem + L::OFF_SETS);
   bool alive = true;
   float ds_sum[2] = {0.f, 0.f};       // queries: the row's rounded dS, two sums
+  float top = 0.f;                    // queries: RowParts::top, at
+  int top_at = 0;
   for (int j = 0; j < t.n_steps; ++j) {
     const int buf = j & (L::SB - 1);
     if (KEYS && L::SB == 2) {
@@ -520,6 +508,24 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
       uint32_t pk[kCols / 2];
       store_packed(s_col + buf * BN, r, pk);
       warp_arrive(bars.s_done + buf, lane);
+    } else {
+      float most[2] = {0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < kCols; c += 4) {
+        most[0] = fmax3(most[0], __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+        most[1] = fmax3(most[1], __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
+      }
+      most[0] = fmaxf(most[0], most[1]);
+      if (most[0] > top) {
+        top = most[0];
+        top_at = static_cast<int>(e & kPiece);
+        if (top >= 0.5f || !(e & kWhole)) {
+          const int key0 = top_at * 64 + in_piece;
+#pragma unroll
+          for (int c = kCols - 1; c >= 0; --c)
+            if (__uint_as_float(r[c]) == top) top_at = ~(key0 + c);
+        }
+      }
     }
     alive = warp_wait(bars.dp_full, j & 1, wl, a.status, abort_flag);
     if (!alive) break;
@@ -539,11 +545,6 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
     }
   }
   // ---- the rows' sums
-  bool sums = alive && t.n_steps > 0;
-  if (sums) {
-    sums = warp_wait(bars.drain, 0, wl, a.status, abort_flag);
-    tc_fence_after();
-  }
   // Two warpgroups take a panel of 64 columns at a time: 32 columns a thread,
   // rounded, into the first operand's ring (every product is done) in the
   // swizzle of its tensor map, then one TMA store, which leaves out rows past
@@ -551,13 +552,56 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
   // dv of d = 128.)
   constexpr int PANELS = (KEYS ? 2 : 1) * (D / 64);
   const int pr = wg >> 1;
-  KeyMean<D>* m = reinterpret_cast<KeyMean<D>*>(smem + L::OFF_R1);
-  float off_zero = 0.f;
+  float off_zero = 0.f, mean[32];
   if (!KEYS) {
-    m->row_sums[wg][row] = ds_sum[0] + ds_sum[1];
+    RowParts* m = reinterpret_cast<RowParts*>(smem + L::OFF_R1);
+    m->sum[wg][row] = ds_sum[0] + ds_sum[1];
+    m->top[wg][row] = top;
+    m->at[wg][row] = top_at;
     named_bar_sync(4, kGroups * 128);
+    top = 0.f;
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) off_zero += m->row_sums[i][row];
+    for (int i = 0; i < kGroups; ++i) {
+      off_zero += m->sum[i][row];
+      if (m->top[i][row] > top) {
+        top = m->top[i][row];
+        top_at = m->at[i][row];
+      }
+    }
+    // on their way while the last products run
+    if (pr < PANELS) {
+      const int at = pr * 64 + (wg & 1) * 32;
+      if (top_at >= 0) {
+        const float4* src = reinterpret_cast<const float4*>(a.k_means + (t.bh * (a.Npad / 64) + top_at) * D + at);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 x = src[j];
+          mean[4 * j] = x.x;
+          mean[4 * j + 1] = x.y;
+          mean[4 * j + 2] = x.z;
+          mean[4 * j + 3] = x.w;
+        }
+      } else {
+        const GradStride& st = a.st[kK];
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + t.b * st.b + t.h * st.h +
+                                                          ~top_at * st.n + at);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 x = __ldg(src + j);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mean[8 * j + 2 * i] = __uint_as_float(w[i] << 16);
+            mean[8 * j + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+          }
+        }
+      }
+    }
+  }
+  bool sums = alive && t.n_steps > 0;
+  if (sums) {
+    sums = warp_wait(bars.drain, 0, wl, a.status, abort_flag);
+    tc_fence_after();
   }
   for (int i = pr; i < PANELS; i += 2) {
     const int acc = i / (D / 64), c64 = (i % (D / 64)) * 64;
@@ -571,7 +615,6 @@ __device__ __forceinline__ void softmax(uint8_t* smem, const Bars& bars, uint32_
       for (int j = 0; j < 32; ++j) o[j] = 0u;
     }
     if (!KEYS && sums) {
-      const float* mean = m->mean[half] + c64 + (wg & 1) * 32;
 #pragma unroll
       for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(fmaf(-off_zero, mean[j], __uint_as_float(o[j])));
     }
@@ -656,7 +699,6 @@ __device__ __forceinline__ void run_tile(uint8_t* smem, const CUtensorMap* tq, c
       else produce<D, KEYS, MASKED>(smem, bars, tk, tv, a, t, walk, entries, abort_flag);
     }
   } else {
-    if (!KEYS && warp < 2) nearest_keys<D>(reinterpret_cast<KeyMean<D>*>(smem + L::OFF_R1), a, t, row0, row1, shift);
     if (threadIdx.x < 128) {
       int n = 0;
       for (int w = threadIdx.x; w < W; w += 128) n += __popc(row0[w] | (row1 ? row1[w] : 0u));

@@ -42,7 +42,7 @@ struct AttendGradArgs {
   const int32_t* cols;
   const uint64_t* masks;        // per-token scope, as AttendArgs::masks
   int32_t* status;
-  const void *q, *k, *dout;     // bf16: a query tile's own rows are read without a tensor map, k's sums taken
+  const void *q, *k, *dout;     // bf16: a query tile's own rows are read without a tensor map, k's means taken
   void *dq, *dk, *dv;           // fp32; bf16 gradients leave through tensor maps
   GradStride st[kGradTensors];
   long long wait_limit;
@@ -50,7 +50,7 @@ struct AttendGradArgs {
   int Npad;                     // N_valid rounded up to whole 128-row tiles
   float* neg_lse2;              // [B*H][Npad] -lse in log2 units; -inf: the row keeps nothing
   float* neg_delta;             // [B*H][Npad] -sum of dout * out
-  float* k_sums;                // bf16: [B*H][Npad / 64][d] k summed over each 64 rows
+  float* k_means;               // bf16: [B*H][Npad / 64][d] mean of each 64 keys, or 0 where they have little in common
   uint32_t* bits;               // [B*H][nB queries][ceil(nB / 32)] kept key blocks
   uint32_t* bits_t;             // [B*H][nB keys][ceil(nB / 32)] query blocks that keep it
   uint64_t* masks_t;            // [B*H][nB keys][nB queries], written where bits are set

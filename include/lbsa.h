@@ -279,8 +279,8 @@ int lbsa_attend(const void* q, const void* k, const void* v, const lbsa_qkv_desc
  * another row of its 128-row tile keeps the block, as in lbsa_attend, and one
  * of a query block a key block in the same way.
  * Limits: B <= 32767, H <= 65535 (LBSA_ERR_UNSUPPORTED beyond).
- * Scratch: 8 bytes a padded row, two bits a block pair, for per-token
- * blocksets 8 bytes a block pair, from the library pool. */
+ * Scratch, from the library pool: 8 bytes a padded row (bf16: 8 + d / 16), two
+ * bits a block pair, for per-token blocksets 8 bytes a block pair. */
 int lbsa_attend_backward(const void* q, const void* k, const void* v, const void* out, const void* dout,
                          const float* lse, const lbsa_qkv_desc* desc, const int64_t* strides,
                          const lbsa_blockset* bs, void* dq, void* dk, void* dv, void* stream);
