@@ -20,7 +20,9 @@ C ABI's names (``include/lbsa.h``):
 
 Tensors are [B, H, N_valid, d] with a contiguous last dim, bf16 or fp32, on
 the current CUDA device.  There is no CPU fallback: a missing library or a
-missing GPU raises.
+missing GPU raises.  A call runs on the current stream, or on `stream`: then
+its new tensors belong to that stream, as those that torch allocates under
+torch.cuda.stream(stream) do.
 """
 from __future__ import annotations
 
@@ -144,6 +146,28 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+# Memory that the current stream still reads is not given to a call on another
+# stream, nor taken back while that one writes it.
+def _pool(stream):
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
+def _empty_like(x, stream, dtype=None):
+    if stream is None:
+        return torch.empty_like(x, dtype=dtype)
+    with _pool(stream):
+        return torch.empty_like(x, dtype=dtype)
+
+
+def _empty(*shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    with _pool(stream):
+        return torch.empty(*shape, dtype=dtype, device=device)
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
@@ -216,9 +240,9 @@ def lbsa_score(q, k, block: int, mode: str = "exact", scores=None, lse=None, wan
     B, H, N, _ = q.shape
     nB = -(-N // block)
     if scores is None:
-        scores = torch.empty(B, H, N if mode == "meanpool_token" else nB, nB, dtype=torch.float32, device=q.device)
+        scores = _empty(B, H, N if mode == "meanpool_token" else nB, nB, dtype=torch.float32, device=q.device, stream=stream)
     if want_lse and lse is None:
-        lse = torch.empty(B, H, N, dtype=torch.float32, device=q.device)
+        lse = _empty(B, H, N, dtype=torch.float32, device=q.device, stream=stream)
     _on_device(scores, "scores", torch.float32, B * H * (N if mode == "meanpool_token" else nB) * nB)
     _on_device(lse, "lse", torch.float32, B * H * N)
     _check(load_library().lbsa_score(_ptr(q), _ptr(k), ctypes.byref(desc), block, _MODES[mode],
@@ -295,13 +319,13 @@ def lbsa_score_attend(q, k, v, block: int, scores=None, out=None, lse=None, want
     B, H, N, _ = q.shape
     nB = -(-N // block)
     if scores is None:
-        scores = torch.empty(B, H, nB, nB, dtype=torch.float32, device=q.device)
+        scores = _empty(B, H, nB, nB, dtype=torch.float32, device=q.device, stream=stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     else:
         _same_layout(q, out)
     if want_lse and lse is None:
-        lse = torch.empty(B, H, N, dtype=torch.float32, device=q.device)
+        lse = _empty(B, H, N, dtype=torch.float32, device=q.device, stream=stream)
     desc = _desc(q)
     _on_device(scores, "scores", torch.float32, B * H * nB * nB)
     _on_device(lse, "lse", torch.float32, B * H * N)
@@ -343,8 +367,8 @@ def lbsa_select_routed(scores, block: int, p: float, entropy_threshold: float, g
     B, H, nB, nB2 = scores.shape
     if nB != nB2:
         raise LbsaError(LBSA_ERR_INVALID_ARG, "scores must be square per head")
-    ent = torch.empty(B, H, dtype=torch.float64, device=scores.device)
-    dom = torch.empty(B, H, dtype=torch.int32, device=scores.device)
+    ent = _empty(B, H, dtype=torch.float64, device=scores.device, stream=stream)
+    dom = _empty(B, H, dtype=torch.int32, device=scores.device, stream=stream)
     h = ctypes.c_void_p()
     _check(load_library().lbsa_select_routed(_ptr(scores), B, H, nB, block, float(p), float(entropy_threshold),
                                              int(group), _ptr(ent), _ptr(dom), ctypes.byref(h), _stream(stream)))
@@ -356,11 +380,11 @@ def lbsa_attend(q, k, v, bs: Blockset, out=None, lse=None, want_lse=False, strea
     _same_layout(q, k)
     _same_layout(q, v)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     else:
         _same_layout(q, out)
     if want_lse and lse is None:
-        lse = torch.empty(q.shape[0], q.shape[1], q.shape[2], dtype=torch.float32, device=q.device)
+        lse = _empty(q.shape[0], q.shape[1], q.shape[2], dtype=torch.float32, device=q.device, stream=stream)
     desc = _desc(q)
     _on_device(lse, "lse", torch.float32, q.shape[0] * q.shape[1] * q.shape[2])
     _check(load_library().lbsa_attend(_ptr(q), _ptr(k), _ptr(v), ctypes.byref(desc), bs.handle,
@@ -384,9 +408,9 @@ def lbsa_attend_backward(q, k, v, bs: Blockset, out, lse, dout, dq=None, dk=None
     if device < 0 or device != torch.cuda.current_device():
         _on_device(q, "q", contiguous=False)
     B, H, N, d = shape
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _empty_like(q, stream) if dq is None else dq
+    dk = _empty_like(k, stream) if dk is None else dk
+    dv = _empty_like(v, stream) if dv is None else dv
     strides = []
     for t in (q, k, v, out, dout, dq, dk, dv):
         st = t.stride()
@@ -418,8 +442,8 @@ def lbsa_blockset_export(bs: Blockset, stream=None):
     """Compact CSR (row_ptr [R+1], col [nnz]) as int32 device tensors."""
     R = bs.B * bs.H * bs.nB
     dev = torch.device("cuda", torch.cuda.current_device())
-    row_ptr = torch.empty(R + 1, dtype=torch.int32, device=dev)
-    col = torch.empty(max(R * bs.nB, 1), dtype=torch.int32, device=dev)
+    row_ptr = _empty(R + 1, dtype=torch.int32, device=dev, stream=stream)
+    col = _empty(max(R * bs.nB, 1), dtype=torch.int32, device=dev, stream=stream)
     nnz = ctypes.c_int64()
     _check(load_library().lbsa_blockset_export(bs.handle, _ptr(row_ptr), _ptr(col), ctypes.byref(nnz),
                                                _stream(stream)))
@@ -454,7 +478,7 @@ def lbsa_blockset_export_bitmask(bs: Blockset, stream=None):
     device (the bits of uint32 words), bit j % 32 of word j // 32 of a row set
     when key block j is kept."""
     W = (bs.nB + 31) // 32
-    bits = torch.empty(bs.B, bs.H, bs.nB, W, dtype=torch.int32, device=torch.device("cuda", torch.cuda.current_device()))
+    bits = _empty(bs.B, bs.H, bs.nB, W, dtype=torch.int32, device=torch.device("cuda", torch.cuda.current_device()), stream=stream)
     _check(load_library().lbsa_blockset_export_bitmask(bs.handle, _ptr(bits), _stream(stream)))
     return bits
 
@@ -502,7 +526,7 @@ def lbsa_partition_perm(T: int, H: int, W: int, kind: str, tile=(4, 4, 4), frame
         perm = torch.empty(n, dtype=torch.int32)
         _check(lib.lbsa_partition_perm(T, H, W, k, tt, th, tw, _ptr(perm), 0, None))
     else:
-        perm = torch.empty(n, dtype=torch.int32, device=device)
+        perm = _empty(n, dtype=torch.int32, device=device, stream=stream)
         _check(lib.lbsa_partition_perm(T, H, W, k, tt, th, tw, _ptr(perm), 1, _stream(stream)))
     return perm
 
@@ -512,7 +536,7 @@ def lbsa_permute(xs, perm, inverse: bool = False, outs=None, stream=None):
     xs = list(xs)
     for x in xs[1:]:
         _same_layout(xs[0], x)
-    outs = [torch.empty_like(x) for x in xs] if outs is None else list(outs)
+    outs = [_empty_like(x, stream) for x in xs] if outs is None else list(outs)
     for o in outs:
         _same_layout(xs[0], o)
     desc = _desc(xs[0])
@@ -544,7 +568,7 @@ def lbsa_rope_table(grid, dims, theta: float = 10000.0, start=(0.0, 0.0, 0.0), t
     g, m = _three(grid, "grid", ctypes.c_int32), _three(dims, "dims", ctypes.c_int32)
     n = max(sum(e * (r // 2) for e, r in zip(g, m)), 0)
     if table is None:
-        table = torch.empty(n, 2, dtype=torch.float32, device=torch.device("cuda", torch.cuda.current_device()))
+        table = _empty(n, 2, dtype=torch.float32, device=torch.device("cuda", torch.cuda.current_device()), stream=stream)
     _on_device(table, "table", torch.float32, 2 * n)
     _check(load_library().lbsa_rope_table(g, m, float(theta), _three(start, "start", ctypes.c_double), _ptr(table),
                                           _stream(stream)))
@@ -577,7 +601,7 @@ def _rope_call(xs, ys, dys, weights, dweights, table, grid, dims, layout, perm, 
         _on_device(first, "x", contiguous=False)
     outs, packed = [], b""
     for i, x in enumerate(xs):
-        y = torch.empty_like(x) if ys is None else ys[i]
+        y = _empty_like(x, stream) if ys is None else ys[i]
         outs.append(y)
         dy = x if dys is None else dys[i]
         shape = x.shape
@@ -651,7 +675,7 @@ def lbsa_norm_rope_backward(dys, xs, weights, table=None, grid=None, dims=None, 
     """Gradients of lbsa_norm_rope from those of its outputs (dys, in block order)
     and its inputs: (dxs in source order, dweights fp32 with None where there is
     no weight).  The same inputs give the same bits on every call."""
-    dws = [None if w is None else torch.empty_like(w, dtype=torch.float32) for w in weights]
+    dws = [None if w is None else _empty_like(w, stream, torch.float32) for w in weights]
     dxs, args, stream = _rope_call(xs, dxs, dys, weights, dws, table, grid, dims, layout, perm, stream)
     _check(load_library().lbsa_norm_rope_backward(*args, float(eps), stream))
     return dxs, dws
@@ -685,9 +709,9 @@ def lbsa_select_head_noalloc(scores, p: float, counts=None, cols=None, status=No
         raise LbsaError(LBSA_ERR_INVALID_ARG, "scores must be [B, H, nB, nB]")
     B, H, nB, _ = scores.shape
     dev = scores.device
-    counts = torch.empty(B * H * nB, dtype=torch.int32, device=dev) if counts is None else counts
-    cols = torch.empty(B * H * nB * nB, dtype=torch.int32, device=dev) if cols is None else cols
-    status = torch.empty(1, dtype=torch.int32, device=dev) if status is None else status
+    counts = _empty(B * H * nB, dtype=torch.int32, device=dev, stream=stream) if counts is None else counts
+    cols = _empty(B * H * nB * nB, dtype=torch.int32, device=dev, stream=stream) if cols is None else cols
+    status = _empty(1, dtype=torch.int32, device=dev, stream=stream) if status is None else status
     _on_device(counts, "counts", torch.int32, B * H * nB)
     _on_device(cols, "cols", torch.int32, B * H * nB * nB)
     _on_device(status, "status", torch.int32, 1)
