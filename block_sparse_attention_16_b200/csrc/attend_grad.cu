@@ -95,7 +95,8 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
           raise_status(a.status, LBSA_ERR_BAD_INDEX);
           continue;
         }
-        atomicOr(&bm[(i0 + r - w * 32) * W + (j[r] >> 5)], 1u << (j[r] & 31));
+        const uint32_t bit = 1u << (j[r] & 31);
+        if (atomicOr(&bm[(i0 + r - w * 32) * W + (j[r] >> 5)], bit) & bit) raise_status(a.status, LBSA_ERR_BAD_INDEX);   // named twice
         if (a.masks) a.masks_t[(bh * a.nB + j[r]) * a.nB + i0 + r] = set[r];
       }
     }

@@ -274,7 +274,9 @@ int lbsa_attend(const void* q, const void* k, const void* v, const lbsa_qkv_desc
  * nothing (lse = -inf) gives and gets no gradient; a key block that no query
  * keeps gets 0.  bf16: products on bf16 operands (P and dS rounded once), sums
  * in fp32.  The sums are taken in a fixed order: the same inputs give the same
- * bits.  Rows past N_valid are never read and never written.  A non-finite
+ * bits.  Rows past N_valid are never read and never written.  A block id out of
+ * range is skipped, one that a list names twice counts once (in lbsa_attend
+ * twice); both raise LBSA_ERR_BAD_INDEX in bs's status word.  A non-finite
  * element of a key block that a row does not keep can reach that row when
  * another row of its 128-row tile keeps the block, as in lbsa_attend, and one
  * of a query block a key block in the same way.
@@ -310,7 +312,7 @@ int lbsa_blockset_export(const lbsa_blockset* bs, int32_t* row_ptr, int32_t* col
                          void* stream);
 
 /* Build a blockset from a caller CSR (device int32 row_ptr [R+1], col [nnz];
- * lists must be ascending), e.g. frozen indices saved by an earlier run.
+ * lists must be ascending, no id twice), e.g. frozen indices saved by an earlier run.
  * Copies the data; ids are validated on the device (status word).  row_ptr
  * must be a valid CSR offset array (row_ptr[0] = 0, non-decreasing, row_ptr[R]
  * <= the length of col): the copy reads col through it unchecked, and a row
