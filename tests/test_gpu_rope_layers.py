@@ -79,3 +79,23 @@ def test_many_heads_and_tokens(B, Hq, Hk, d, dims, layout, dtype, weights):
         assert dws[i].dtype == torch.float32 and dws[i].shape == ws[i].shape
         _within(host(dws[i]), rdw, 64 * E * total)
         assert torch.equal(dws[i], again[1][i]) and torch.equal(dxs[i], again[0][i])
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_gradients_without_an_eps(dtype, per_head):
+    # five heads in batches of two or four and a ragged last tile: rows that are not there have 1 / sqrt(0)
+    n, d = 2407, 128
+    x, dy = _normal(1, 1, 5, n, d, dtype=dtype), _normal(2, 1, 5, n, d, dtype=dtype)
+    w = 1 + 0.2 * _normal(3, *((5, d) if per_head else (d,)))
+    y, = lbsa.lbsa_norm_rope([x], [w], eps=0.0)
+    (dx,), (dw,) = lbsa.lbsa_norm_rope_backward([dy], [x], [w], eps=0.0)
+    x64, dy64, w64 = (host(t).astype(np.float64) for t in (x, dy, w))
+    ref = oracle.norm_rope(x64, w64, eps=0.0)
+    _within(host(y), ref, (HALF[dtype] + 24 * E) * np.abs(ref))
+    rdx, rdw = oracle.norm_rope_grad(dy64, x64, w64, eps=0.0)
+    r = 1 / np.sqrt((x64 * x64).mean(-1, keepdims=True))
+    nrm, wr = x64 * r, (w64[:, None] if per_head else w64)
+    slack = 32 * E * r * (np.abs(dy64 * wr) + np.abs(nrm) * np.abs(dy64 * wr * nrm).mean(-1, keepdims=True))
+    _within(host(dx), rdx, HALF[dtype] * np.abs(rdx) + slack)
+    _within(host(dw), rdw, 64 * E * np.abs(dy64 * nrm).sum((0, 2) if per_head else (0, 1, 2)))
