@@ -196,11 +196,12 @@ attend_grad_prep_kernel(const T* __restrict__ out, const T* __restrict__ dout, c
 // stand R / 8 x 16 x 64 / R: thread (ty, tx, kz) takes rows ty + R / 8 i and
 // columns tx + 16 j over its share of the elements (the 64 / R threads of a
 // share sum by shuffles).
-// Bound by shared-memory reads: 8 x 4 results take 12 vectors for 128 FMAs,
-// where FMA issue would cover 8.  (With one group of 256 threads, 4 x 4 results
-// took 8 for 64: 2,600 tokens, 4 heads of 128, half of the blocks, 0.89 ms
-// against 0.82.)  24 such heads: 4.0 ms, 37 TFLOP/s of the seven products, half
-// of what the FMA pipes can do.
+// No pipe is full: 8 x 4 results take 12 shared-memory vectors for 128 FMAs, where
+// FMA issue would cover 8, and 8 warps an SM leave gaps: with 24 heads of 128,
+// 2,600 tokens, half of the blocks, FMA 57 %, shared memory 53 %, issue 66 %, and
+// 3.9 ms, 38 TFLOP/s of the seven products, half of what the FMA pipes can do.
+// (With one group of 256 threads, 4 x 4 results took 8 vectors for 64 FMAs: 4 such
+// heads 0.89 ms against 0.82.)
 // R = 64 wherever that fills the SMs; with fewer rows R = 32 or 16 spreads them
 // over more CTAs.  A call with R = 64 / 32 / 16: 41 / 31 / 27 us for 256 tokens,
 // 2 heads of 64 (16 CTAs with R = 64), 200 / 151 / 191 us for 1,000 tokens,

@@ -207,9 +207,9 @@ __device__ __forceinline__ Unit unit_of(const RopeArgs& a, int y) {
 
 // What a unit's rows need is known to the compiler, so that a batch's rows are
 // worked on side by side, without a branch between them: for a layer's q, k, v
-// (21 x 30 x 52 tokens, 12 heads of 128, bf16) the call takes 99 us, 105 us
+// (21 x 30 x 52 tokens, 12 heads of 128, bf16) the call takes 99 to 102 us, 105
 // where the kernel asks row by row.  A weight row for each head is read again
-// for each row (120 us), as eight more registers a head would not fit.
+// for each row (122 us), as eight more registers a head would not fit.
 template <typename T, int D, bool HALF, bool NORM, bool ROTATE, bool PER_HEAD>
 __device__ __forceinline__ void rope_rows(const RopeArgs& a, const RopeItem& it, const Unit& u) {
   constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
@@ -318,14 +318,18 @@ __device__ __forceinline__ void async_row(uint32_t dst, const T* src, int gap, b
 // source order.  A thread's rows come through its own slots of shared memory,
 // kStages - 1 batches ahead (another's slots are read within a half-split row
 // only).  For a layer's q, k, v (21 x 30 x 52 tokens, 12 heads of 128, bf16), for
-// which memory needs 123 us, the kernel takes 133 us and the call 137-143 us
-// (151 us where the kernel asks row by row what a unit needs; 168 us with the
-// next batch in registers).  Half-split rows: 143 us (172 us with pairs that are
-// exchanged between lanes, 171 us with copies of 8 bytes).
+// which memory needs 123 us, the kernel takes 133 us and the call 142 to 153 us.
+// (Side by side, each from one run: 139 us, 151 where the kernel asks row by row
+// what a unit needs, 168 with the next batch in registers; half-split rows 143 us,
+// 172 with pairs that are exchanged between lanes, 171 with copies of 8 bytes.)
+// fp32 rows need 246 us: half-split 257 us, interleaved 394, where each of a lane's
+// two 16-byte copies takes every second half of a 32-byte sector (no counters).
 // A thread adds its columns' du n over all its rows; the block adds its groups'
 // sums in a fixed order and writes one partial row, so the weight gradient does
 // not depend on the order in which blocks run.  With a weight row for each head
-// a unit is one batch of heads, with a sum each: 200 us, 305 us with one head.
+// a unit is one batch of heads, with a sum each: 216 us (one head: 305), half-split
+// 236, fp32 364 and interleaved 690; a token's place and angles are looked up
+// again for every batch.
 constexpr int kStages = 4;
 constexpr int kStageVecs = 4;                    // 16-byte slots of a thread in a stage: 64 bytes of x and dy
 // heads of a token that a thread works on together

@@ -342,7 +342,7 @@ int lbsa_blockset_from_bitmask(const uint32_t* bits, int32_t B, int32_t H, int32
 int lbsa_get_status(const lbsa_blockset* bs, int32_t* device_status, int32_t clear, void* stream);
 
 /* Per-device status word of calls that have no blockset (lbsa_score,
- * lbsa_permute).  Synchronises the stream. */
+ * lbsa_permute, lbsa_rope and the two norm calls).  Synchronises the stream. */
 int lbsa_device_status(int32_t* device_status, int32_t clear, void* stream);
 
 /* Token order of a (T, Hg, Wg) grid for one block partition (VMoBA review:
@@ -423,7 +423,9 @@ int lbsa_rope_table(const int32_t* grid, const int32_t* dims, double theta, cons
  * its gradient.  perm as in lbsa_permute: an entry outside [0, N) skips its
  * row and records LBSA_ERR_BAD_INDEX in the per-device status word.  No y may
  * alias an input or another y of the call.  Products and sums in fp32, rounded
- * once. */
+ * once.
+ * Limit, here and in the two calls below: B times the heads of all tensors
+ * <= 65535 (LBSA_ERR_UNSUPPORTED beyond). */
 int lbsa_rope(const lbsa_rope_item* items, int32_t count, int32_t B, int32_t N, int32_t d, int32_t dtype,
               const lbsa_rope_pos* pos, const int32_t* perm, int32_t inverse, void* stream);
 
@@ -440,8 +442,9 @@ int lbsa_norm_rope(const lbsa_rope_item* items, int32_t count, int32_t B, int32_
  * a fixed order (fp32 within a block of rows, 64 bits across blocks), so
  * repeated calls give the same bits.  A weight that two tensors share has a
  * dweight for each.  Scratch, from the library pool: one fp32 row of d (bf16
- * tensors: two) for each block of the launch, of which there are about 1,300
- * or, with more (batch, head) pairs than that, one for each. */
+ * tensors: two) for each block of the launch.  A unit is up to 16 heads of one
+ * tensor and batch element (with a weight row for each head one, bf16 two);
+ * there are fewer than 1,332 + units blocks. */
 int lbsa_norm_rope_backward(const lbsa_rope_item* items, int32_t count, int32_t B, int32_t N, int32_t d,
                             int32_t dtype, const lbsa_rope_pos* pos, const int32_t* perm, double eps, void* stream);
 
